@@ -349,6 +349,65 @@ dma_status_t dma_cp_compact(const dma_params_t* p, int32_t prefix_len, int32_t n
                             void* stream);
 
 /*
+ * From the projections to the attention's inputs: per-head norm of queries and keys, position rotation
+ * and transposition in one pass, with its backward.  Where the o_t equation's q and k come from is left
+ * open by the page; this is the usual step in front of it.
+ *
+ * For a head row x [d] of a query (key) at position n:
+ *   y = x (mean(x^2) + eps)^(-1/2) weight     (q_weight / k_weight [d] dtype; NULL: y = x)
+ *   the first `rot` channels of y are rotated in pairs, pair i by the angle n inv_freq[i]:
+ *   (a, b) -> (a cos - b sin, b cos + a sin), the pair being channels (i, i + rot/2), or
+ *   (2i, 2i + 1) when `interleaved` is 1.  Angles are formed in double precision and every result is
+ *   rounded once.  Value rows are copied.
+ * Position n of row (b, i): positions[b * N + i] where given, else first + i.
+ *   rot       0 .. d, a multiple of 16; inv_freq (float32 [rot/2], radians per position) NULL iff rot == 0
+ *   eps       finite, > 0
+ */
+typedef struct {
+  const float* inv_freq;
+  const int32_t* positions; /* [B, N] or NULL */
+  const void* q_weight;
+  const void* k_weight;
+  float eps;
+  int32_t rot;
+  int32_t interleaved;
+  int32_t first;
+} dma_prep_t;
+
+/* Element strides of the projections' tensors, {batch, position, head}; the d channels of a row are
+ * contiguous.  Each is non-negative and a multiple of 16 bytes.  Projections as they come out of one
+ * product, [B, N, H + 2 Hkv, d], or of three, or head-major, are all described by it. */
+typedef struct {
+  int64_t q[3], k[3], v[3];
+} dma_prep_strides_t;
+
+/*
+ * Forward.  q, k, v: strided as st says (H, Hkv, Hkv heads of d channels, dtype).  Out: Q [B, H, N, d],
+ * K, V [B, Hkv, N, d] dtype, dense.  v and V may be NULL together.  p: B, H, Hkv, N, d and dtype are
+ * used, Nq must equal N; N <= 2^24 (no other limit of the attention applies).  Outputs must not overlap inputs.
+ */
+dma_status_t dma_prep(const dma_params_t* p, const dma_prep_t* r, const dma_prep_strides_t* st, const void* q,
+                      const void* k, const void* v, void* Q, void* K, void* V, void* stream);
+
+/* Bytes of workspace of dma_prep_bwd. */
+dma_status_t dma_prep_workspace_size(const dma_params_t* p, const dma_prep_t* r, size_t* bytes);
+
+/*
+ * Backward.  q, k: the forward's inputs, strided as st says (each may be NULL when its weight is: then it
+ * is not read).
+ * dQ, dK, dV: gradients of the forward's outputs, dense, dtype; dV_gate [B, Hkv, N, d] float32 or NULL is
+ * added to dV before the one rounding (the gate's share from dma_gate_bwd).
+ * Out: dq, dk, dv, strided as gst says, dtype (rows must not overlap one another: DMA_ERR_INVALID_ARG);
+ * what lies between the rows is left as it is.  dV and dv may be NULL together (dV_gate too, then).
+ * dq_weight, dk_weight [d] float32, sums over every row; each may be NULL, and must be where the weight
+ * is.  The sums do not depend on scheduling: two runs give the same bits.
+ */
+dma_status_t dma_prep_bwd(const dma_params_t* p, const dma_prep_t* r, const dma_prep_strides_t* st,
+                          const dma_prep_strides_t* gst, const void* q, const void* k, const void* dQ,
+                          const void* dK, const void* dV, const float* dV_gate, void* dq, void* dk, void* dv,
+                          float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Reads the device status word of `workspace` (synchronises `stream`).  Returns DMA_OK or
  * DMA_ERR_TIMEOUT when a kernel's bounded wait gave up; *code receives the raw word.
  * dma_clear_device_status resets it (asynchronously on `stream`).

@@ -13,8 +13,8 @@ from __future__ import annotations
 
 import ctypes
 
-from ._lib import (BLOCK_Q, DMA_BF16, DMA_F32, DMA_FLAG_FORWARD_ONLY, DmaCpLayout, DmaError, DmaParams, DmaWsLayout,
-                   LIB_PATH, check, exported_names, load)
+from ._lib import (BLOCK_Q, DMA_BF16, DMA_F32, DMA_FLAG_FORWARD_ONLY, DmaCpLayout, DmaError, DmaParams, DmaPrep,
+                   DmaPrepStrides, DmaWsLayout, LIB_PATH, check, exported_names, load)
 
 __all__ = [
     "BLOCK_Q", "DMA_BF16", "DMA_F32", "DmaError", "DmaParams", "LIB_PATH", "load", "exported_names",
@@ -23,6 +23,7 @@ __all__ = [
     "gate_bwd", "gate_bwd_noalloc", "check_device_status", "clear_device_status", "selftest_bounded_wait",
     "abi_version", "alloc_workspace", "forward",
     "backward", "cp_layout", "cp_candidates", "cp_compact",
+    "DmaPrep", "make_prep", "prep", "prep_bwd", "prep_workspace_size", "alloc_prep_workspace",
 ]
 
 
@@ -174,7 +175,118 @@ def cp_compact(p, prefix_len, n_prev, cands, delta, K, V, delta_c, Kc, Vc, pos_c
                                                   _nbytes(workspace), _stream(stream)))
 
 
+# ---------------------------------------------------------------- projections to inputs
+
+def _here(*tensors):
+    """Every tensor given (None and raw addresses aside) lies on the current CUDA device."""
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and not isinstance(t, int) and t.get_device() != dev:
+            raise ValueError(f"tensors passed to libdma must be on the current device (cuda:{dev}); got {t.device}")
+
+
+def _shaped(name, t, shape, p=None):
+    """t (a tensor, or None) has the given shape and, with p, p's storage type; without, float32."""
+    if t is None or isinstance(t, int):
+        return
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have the shape {shape}, not {tuple(t.shape)}")
+    want = "torch.bfloat16" if p is not None and p.dtype == DMA_BF16 else "torch.float32"
+    if str(t.dtype) != want:
+        raise ValueError(f"{name} must be {want}, not {t.dtype}")
+
+
+def _rows_ptr(name, t, shape, out, p):
+    """Address of a strided tensor of rows [.., heads, d]; its strides (all but the last) go into out."""
+    if t is None:
+        return None
+    _shaped(name, t, shape, p)
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError(f"{name}: the channels of a row must be contiguous")
+    n = len(shape) - 1
+    for i in range(n):
+        out[3 - n + i] = st[i] if shape[i] > 1 else 0
+    return t.data_ptr()
+
+
+def make_prep(inv_freq, q_weight=None, k_weight=None, eps=1e-6, positions=None, first=0, interleaved=False) -> DmaPrep:
+    """dma_prep_t: the norm and rotation between the projections and the attention.
+
+    inv_freq: device float32 [rot / 2] (radians per position), rotating the first rot
+    channels; None: no rotation.  q_weight, k_weight: [d] in the storage type; None: no
+    norm.  positions: device int32 [B, N]; None: first, first + 1, ...  interleaved: the
+    pairs are neighbouring channels instead of the two halves.  The result keeps the
+    tensors alive."""
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    r = DmaPrep(inv_freq=_ptr(inv_freq), positions=_ptr(positions), q_weight=_ptr(q_weight), k_weight=_ptr(k_weight),
+                eps=float(eps), rot=rot, interleaved=1 if interleaved else 0, first=int(first))
+    _shaped("inv_freq", inv_freq, (rot // 2,))
+    if positions is not None and str(positions.dtype) != "torch.int32":
+        raise ValueError(f"positions must be torch.int32, not {positions.dtype}")
+    r.tensors = (inv_freq, q_weight, k_weight, positions)
+    return r
+
+
+def _check_prep_tensors(p, r):
+    _, qw, kw, pos = r.tensors
+    _shaped("q_weight", qw, (p.d,), p)
+    _shaped("k_weight", kw, (p.d,), p)
+    if pos is not None and tuple(pos.shape) != (p.B, p.N):
+        raise ValueError(f"positions must have the shape {(p.B, p.N)}, not {tuple(pos.shape)}")
+
+
+def prep(p, r, q, k, v, Q, K, V, stream=None):
+    """Projections q [B, N, H, d], k, v [B, N, Hkv, d] (any strides) to the attention's inputs
+    Q [B, H, N, d], K, V [B, Hkv, N, d]: per-head norm, rotation and transposition in one pass.
+    v and V may be None together."""
+    _here(q, k, v, Q, K, V, *r.tensors)
+    _check_prep_tensors(p, r)
+    st = DmaPrepStrides()
+    qp = _rows_ptr("q", q, (p.B, p.N, p.H, p.d), st.q, p)
+    kp = _rows_ptr("k", k, (p.B, p.N, p.Hkv, p.d), st.k, p)
+    vp = _rows_ptr("v", v, (p.B, p.N, p.Hkv, p.d), st.v, p)
+    _shaped("Q", Q, (p.B, p.H, p.N, p.d), p)
+    _shaped("K", K, (p.B, p.Hkv, p.N, p.d), p)
+    _shaped("V", V, (p.B, p.Hkv, p.N, p.d), p)
+    check("dma_prep", load().dma_prep(ctypes.byref(p), ctypes.byref(r), ctypes.byref(st), qp, kp, vp, _ptr(Q), _ptr(K),
+                                      _ptr(V), _stream(stream)))
+
+
+def prep_workspace_size(p, r) -> int:
+    n = ctypes.c_size_t(0)
+    check("dma_prep_workspace_size", load().dma_prep_workspace_size(ctypes.byref(p), ctypes.byref(r), ctypes.byref(n)))
+    return int(n.value)
+
+
+def prep_bwd(p, r, q, k, dQ, dK, dV, dV_gate, dq, dk, dv, dq_weight, dk_weight, workspace, stream=None):
+    """Gradients of prep's inputs from those of its outputs: dq, dk, dv are written at their own
+    strides ([B, N, heads, d]), dV_gate (float32, or None) is added to dV, dq_weight and dk_weight are
+    float32 [d] (None: not wanted); q, k as in prep (None where there is no weight)."""
+    _here(q, k, dQ, dK, dV, dV_gate, dq, dk, dv, dq_weight, dk_weight, workspace, *r.tensors)
+    _check_prep_tensors(p, r)
+    st, gst = DmaPrepStrides(), DmaPrepStrides()
+    sq, sk = (p.B, p.N, p.H, p.d), (p.B, p.N, p.Hkv, p.d)
+    ptrs = [_rows_ptr("dq", dq, sq, gst.q, p), _rows_ptr("dk", dk, sk, gst.k, p), _rows_ptr("dv", dv, sk, gst.v, p)]
+    qp, kp = _rows_ptr("q", q, sq, st.q, p), _rows_ptr("k", k, sk, st.k, p)
+    _shaped("dQ", dQ, (p.B, p.H, p.N, p.d), p)
+    for name, t, like in (("dK", dK, p), ("dV", dV, p), ("dV_gate", dV_gate, None)):
+        _shaped(name, t, (p.B, p.Hkv, p.N, p.d), like)
+    _shaped("dq_weight", dq_weight, (p.d,))
+    _shaped("dk_weight", dk_weight, (p.d,))
+    check("dma_prep_bwd", load().dma_prep_bwd(ctypes.byref(p), ctypes.byref(r), ctypes.byref(st), ctypes.byref(gst), qp, kp,
+                                              _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(dV_gate), *ptrs, _ptr(dq_weight),
+                                              _ptr(dk_weight), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
 # ---------------------------------------------------------------- convenience (torch allocation)
+
+def alloc_prep_workspace(p, r, device="cuda"):
+    """A workspace for prep_bwd (torch allocation)."""
+    import torch
+    return torch.empty(prep_workspace_size(p, r), dtype=torch.uint8, device=device)
+
 
 def alloc_workspace(p, device="cuda", stream=None):
     """A workspace for problem p (torch allocation) with its status word cleared."""

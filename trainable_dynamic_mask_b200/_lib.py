@@ -43,6 +43,15 @@ class DmaCpLayout(ctypes.Structure):
                 ("ws_bytes", c_sz), ("off_status", c_sz), ("prefix_rows", c_i32), ("reserved", c_i32)]
 
 
+class DmaPrep(ctypes.Structure):
+    _fields_ = [("inv_freq", c_vp), ("positions", c_vp), ("q_weight", c_vp), ("k_weight", c_vp), ("eps", c_f32),
+                ("rot", c_i32), ("interleaved", c_i32), ("first", c_i32)]
+
+
+class DmaPrepStrides(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_int64 * 3), ("k", ctypes.c_int64 * 3), ("v", ctypes.c_int64 * 3)]
+
+
 # name -> argtypes (every function returns dma_status_t as int32 unless listed in _RESTYPES)
 _SIGS = {
     "dma_status_string": [c_i32],
@@ -68,6 +77,12 @@ _SIGS = {
     "dma_cp_candidates": [ctypes.POINTER(DmaParams), c_i32, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp, c_sz, c_vp],
     "dma_cp_compact": [ctypes.POINTER(DmaParams), c_i32, c_i32, c_vp, c_sz, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
                        c_vp, c_sz, c_vp],
+    "dma_prep": [ctypes.POINTER(DmaParams), ctypes.POINTER(DmaPrep), ctypes.POINTER(DmaPrepStrides), c_vp, c_vp, c_vp,
+                 c_vp, c_vp, c_vp, c_vp],
+    "dma_prep_workspace_size": [ctypes.POINTER(DmaParams), ctypes.POINTER(DmaPrep), ctypes.POINTER(c_sz)],
+    "dma_prep_bwd": [ctypes.POINTER(DmaParams), ctypes.POINTER(DmaPrep), ctypes.POINTER(DmaPrepStrides),
+                     ctypes.POINTER(DmaPrepStrides), c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                     c_vp, c_sz, c_vp],
 }
 _RESTYPES = {"dma_status_string": ctypes.c_char_p, "dma_abi_version": c_i32}
 

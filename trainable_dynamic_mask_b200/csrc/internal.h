@@ -96,6 +96,30 @@ bool make_row_map(void* map, const void* base, uint64_t rows, int d);
 bool make_tile_map(void* map, const void* base, uint64_t rows, int d, int box_rows);
 int sm_count();   // SMs of the current device
 
+// ---------------------------------------------------------------- projections to inputs (prep.cu)
+constexpr int kPrepMaxBlocks = 592;   // 4 blocks an SM: rows of partial sums of the backward's workspace
+// Arguments of the kernels of dma_prep and dma_prep_bwd; [3] = query, key, value.
+struct PrepArgs {
+  const float* inv_freq;
+  const int32_t* positions;
+  const void* weight[2];
+  const void* in[3];        // the projections (backward: q, k)
+  const void* grad[3];      // backward: dQ, dK, dV
+  const float* dv_gate;     // backward
+  void* out[3];             // Q, K, V (backward: dq, dk, dv)
+  float* part;              // backward: partial sums of the weights' gradients [2][blocks][d]
+  long long stride[3][3];   // of the projections: batch, position, head
+  long long gstride[3][3];  // backward: of dq, dk, dv
+  float eps;
+  int B, H, Hkv, N, rot, first;
+  bool inter;
+};
+// Checks of a dma_prep_t that do not depend on the call.
+dma_status_t check_prep(const dma_prep_t* r, int d);
+bool check_strides(const int64_t (&st)[3], bool bf16);
+cudaError_t launch_prep_fwd(const PrepArgs& a, bool bf16, int d, cudaStream_t s);
+cudaError_t launch_prep_bwd(const PrepArgs& a, bool bf16, int d, float* dq_weight, float* dk_weight, cudaStream_t s);
+
 // ---------------------------------------------------------------- launchers (cudaError_t)
 cudaError_t launch_gate_fwd(const Plan& P, const void* V, const void* Delta, const float* A,
                             float* delta, float* x_save, cudaStream_t s);
