@@ -246,7 +246,7 @@ def prepare(case, seed):
     if own:
         import trainable_dynamic_mask_b200 as dma
         st["p"] = dma.make_params(S, H, Hkv, c["longest"], d, c.get("w", 1), Nq=1, dtype=c["dtype"])
-        st["pages"] = dma.make_pages(st["Kp"], st["Vp"], st["dp"], table, st["lens"], prefix=P)
+        st["pages"] = dma.make_pages(st["p"], st["Kp"], st["Vp"], st["dp"], table, st["lens"], prefix=P)
         st["ws"] = dma.alloc_paged_workspace(st["p"], st["pages"])
         if c["op"] == "append":
             st["r"] = dma.make_prep(st["freq"], q_weight=st["qw"], k_weight=st["kw"], eps=EPS, interleaved=c["inter"])
