@@ -408,6 +408,86 @@ dma_status_t dma_prep_bwd(const dma_params_t* p, const dma_prep_t* r, const dma_
                           float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Paged cache: keys, values and gate values of many sequences in fixed-size pages, for serving.  The
+ * selection is the m_t equation's (the best min(len, w) keys of a sequence by delta, ties to the lower
+ * position) and the attention the o_t equation's, for the single query at each sequence's last position;
+ * only where the rows lie differs from dma_topk_mask / dma_attn_fwd with Nq == 1.
+ *
+ * Position j of sequence b lies in slot j % page of page table[b, j / page].  p describes the problem: B
+ * sequences, H, Hkv, d, w, w_heads, scale and dtype as everywhere, Nq == 1, and N = the longest a sequence
+ * may be in any call (it sizes the workspace and the launches; the work follows the lengths).  Lengths and
+ * tables are read on the device, so a captured graph may be replayed as they change.
+ *   K, V     [n_pages, Hkv, page, d] dtype;  delta [n_pages, H, page] float32
+ *   table    int32 [B, max_pages];  lens int32 [B]: cache lengths, tokens being appended included.  A length
+ *            of 0 (or below) is an idle row: nothing is appended, O = 0 and LSE = -inf.
+ *   page     a power of two from 16 to 1024; n_pages * page < 2^31; N <= max_pages * page
+ *   prefix   0, or a multiple of page: the leading positions that every sequence shares: their table entries
+ *            are those of sequence 0 (whose row holds them even if it is idle).  The selection and the
+ *            attention over them are then computed once for the whole batch; the results are those of
+ *            prefix == 0 but for the order of sums.  Every length is then 0 or at least prefix.
+ * A page number outside [0, n_pages), a length above N (or between 0 and prefix) is never followed: the
+ * kernels skip that token or treat that row as idle, and OR 0x10000000 into the status word.
+ * dma_check_device_status and dma_clear_device_status work on this workspace with the same p.
+ * Limits (DMA_ERR_UNSUPPORTED beyond them): those of decode; dma_paged_append: H <= 64.
+ */
+typedef struct {
+  void* K;
+  void* V;
+  float* delta;
+  const int32_t* table;
+  const int32_t* lens;
+  int32_t n_pages, page, max_pages, prefix;
+} dma_pages_t;
+
+/*
+ * Workspace of the paged calls and what may be read from it after dma_paged_topk:
+ *   off_rows  int32 [B, H, 4]: {listed, edge, cut, shared}.  `listed` selected keys are in the row's list;
+ *             with a prefix, `shared` more are candidates of the prefix: candidate i of head h is
+ *             selected iff its delta is above the value whose order key is edge, or equal to it with i < cut.
+ *             The order key of a float f with bits u is u | 2^31 for u < 2^31, else ~u (-0.0 as +0.0).
+ *   off_sel   int32 [B, H, sel_len]: the listed keys' positions, ascending (without a prefix, all selected)
+ *   off_cand  int32 [H, cand_len]: with a prefix, the best min(window, prefix) of its positions, ascending
+ *   the rest  internal scratch.  off_status as in dma_ws_layout_t: clear it once.
+ */
+typedef struct {
+  size_t bytes, off_status, off_rows, off_sel, off_cand;
+  int32_t sel_len, cand_len;
+} dma_paged_layout_t;
+
+dma_status_t dma_paged_layout(const dma_params_t* p, const dma_pages_t* c, dma_paged_layout_t* layout);
+
+/*
+ * Appends tokens to the cache, from their projections: keys normed and rotated (as in dma_prep, r->positions
+ * NULL and r->first ignored: the position is the one in the cache), values copied, gate value formed from the
+ * values (as in dma_gate), and the same tokens' queries normed and rotated into Q.
+ *   T        tokens in q, k, v;  starts: int32 [B + 1] ascending: sequence b appends the tokens starts[b] ..
+ *            starts[b+1]-1 as its last positions (of lens[b]); tokens behind starts[B] are padding.  NULL:
+ *            T == B, one token each.
+ *   q, k, v  strided {-, token, head} as st says (H, Hkv, Hkv heads), dtype;  Q [T, H, d] dtype, dense.  q and
+ *            Q may be NULL together.  Rows of padding, idle rows and skipped tokens are left as they were.
+ *   Delta [Hkv*d, H] dtype, A [H] float32
+ * No two sequences may append to the same slot.  x is accumulated in float32.  The call is complete in the
+ * stream's order like any other; it needs the workspace for its status word only.
+ */
+dma_status_t dma_paged_append(const dma_params_t* p, const dma_pages_t* c, const dma_prep_t* r,
+                              const dma_prep_strides_t* st, int32_t T, const int32_t* starts, const void* q,
+                              const void* k, const void* v, const void* Delta, const float* A, void* Q,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Selection of every row (b, h) over its cache: delta of the pages in, the workspace's lists out. */
+dma_status_t dma_paged_topk(const dma_params_t* p, const dma_pages_t* c, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/*
+ * Attention of one query for each sequence over the keys dma_paged_topk selected (same p, c and workspace;
+ * may be called again for other queries).  Q [B, H, d] dtype; O [B, H, d] dtype out, LSE [B, H] float32 out.
+ * float32 storage is computed in float32 (nothing is rounded to bfloat16).  Its rows, and a batch of one,
+ * are computed one by one whatever prefix is (cand_len is 0 then).
+ */
+dma_status_t dma_paged_attn(const dma_params_t* p, const dma_pages_t* c, const void* Q, void* workspace,
+                            size_t workspace_bytes, void* O, float* LSE, void* stream);
+
+/*
  * Reads the device status word of `workspace` (synchronises `stream`).  Returns DMA_OK or
  * DMA_ERR_TIMEOUT when a kernel's bounded wait gave up; *code receives the raw word.
  * dma_clear_device_status resets it (asynchronously on `stream`).

@@ -13,8 +13,8 @@ from __future__ import annotations
 
 import ctypes
 
-from ._lib import (BLOCK_Q, DMA_BF16, DMA_F32, DMA_FLAG_FORWARD_ONLY, DmaCpLayout, DmaError, DmaParams, DmaPrep,
-                   DmaPrepStrides, DmaWsLayout, LIB_PATH, check, exported_names, load)
+from ._lib import (BLOCK_Q, DMA_BF16, DMA_F32, DMA_FLAG_FORWARD_ONLY, DmaCpLayout, DmaError, DmaPagedLayout, DmaPages, DmaParams,
+                   DmaPrep, DmaPrepStrides, DmaWsLayout, LIB_PATH, check, exported_names, load)
 
 __all__ = [
     "BLOCK_Q", "DMA_BF16", "DMA_F32", "DmaError", "DmaParams", "LIB_PATH", "load", "exported_names",
@@ -24,6 +24,7 @@ __all__ = [
     "abi_version", "alloc_workspace", "forward",
     "backward", "cp_layout", "cp_candidates", "cp_compact",
     "DmaPrep", "make_prep", "prep", "prep_bwd", "prep_workspace_size", "alloc_prep_workspace",
+    "DmaPages", "make_pages", "paged_layout", "paged_append", "paged_topk", "paged_attn", "alloc_paged_workspace",
 ]
 
 
@@ -280,7 +281,84 @@ def prep_bwd(p, r, q, k, dQ, dK, dV, dV_gate, dq, dk, dv, dq_weight, dk_weight, 
                                               _ptr(dk_weight), _ptr(workspace), _nbytes(workspace), _stream(stream)))
 
 
+# ---------------------------------------------------------------- paged cache
+
+def make_pages(p, K, V, delta, table, lens, prefix=0) -> DmaPages:
+    """dma_pages_t: the paged cache of p's sequences.  K, V [n_pages, Hkv, page, d], delta
+    [n_pages, H, page] float32, table int32 [B, max_pages], lens int32 [B] (device tensors, which the
+    result keeps alive; they may be written to between calls).  prefix: leading positions that every
+    sequence shares, a multiple of the page length."""
+    import torch
+    if K.dim() != 4:
+        raise ValueError("K must be [n_pages, Hkv, page, d]")
+    n, _, page, _ = K.shape
+    _here(K, V, delta, table, lens)
+    _shaped("K", K, (n, p.Hkv, page, p.d), p)
+    _shaped("V", V, (n, p.Hkv, page, p.d), p)
+    _shaped("delta", delta, (n, p.H, page))
+    if table.dim() != 2 or table.shape[0] != p.B or tuple(lens.shape) != (p.B,):
+        raise ValueError(f"table must be [{p.B}, max_pages] and lens [{p.B}]")
+    if table.dtype != torch.int32 or lens.dtype != torch.int32:
+        raise ValueError("table and lens must be torch.int32")
+    c = DmaPages(K=_ptr(K), V=_ptr(V), delta=_ptr(delta), table=_ptr(table), lens=_ptr(lens), n_pages=n, page=page,
+                 max_pages=table.shape[1], prefix=int(prefix))
+    c.tensors = (K, V, delta, table, lens)
+    return c
+
+
+def paged_layout(p, c) -> DmaPagedLayout:
+    lay = DmaPagedLayout()
+    check("dma_paged_layout", load().dma_paged_layout(ctypes.byref(p), ctypes.byref(c), ctypes.byref(lay)))
+    return lay
+
+
+def paged_append(p, c, r, q, k, v, Delta, A, Q, workspace, starts=None, stream=None):
+    """Appends tokens to the cache from their projections q [T, H, d], k, v [T, Hkv, d] (any strides),
+    as the last positions of c.lens: K normed and rotated, V, the gate values; Q [T, H, d] receives the
+    normed and rotated queries (q and Q may be None together).  starts: device int32 [B + 1], the
+    sequences' token ranges; None: one token each."""
+    _here(q, k, v, Delta, A, Q, workspace, starts)
+    T = k.shape[0]
+    st = DmaPrepStrides()
+    qp = _rows_ptr("q", q, (T, p.H, p.d), st.q, p)
+    kp = _rows_ptr("k", k, (T, p.Hkv, p.d), st.k, p)
+    vp = _rows_ptr("v", v, (T, p.Hkv, p.d), st.v, p)
+    _shaped("Q", Q, (T, p.H, p.d), p)
+    _shaped("Delta", Delta, (p.Hkv * p.d, p.H), p)
+    _shaped("A", A, (p.H,))
+    _check_prep_tensors(p, r)
+    if starts is not None and (tuple(starts.shape) != (p.B + 1,) or str(starts.dtype) != "torch.int32"):
+        raise ValueError(f"starts must be torch.int32 [{p.B + 1}]")
+    check("dma_paged_append", load().dma_paged_append(ctypes.byref(p), ctypes.byref(c), ctypes.byref(r),
+                                                      ctypes.byref(st), T, _ptr(starts), qp, kp, vp, _ptr(Delta),
+                                                      _ptr(A), _ptr(Q), _ptr(workspace), _nbytes(workspace),
+                                                      _stream(stream)))
+
+
+def paged_topk(p, c, workspace, stream=None):
+    """Selection of every (sequence, head) over its cache, into the workspace."""
+    _here(workspace)
+    check("dma_paged_topk", load().dma_paged_topk(ctypes.byref(p), ctypes.byref(c), _ptr(workspace),
+                                                  _nbytes(workspace), _stream(stream)))
+
+
+def paged_attn(p, c, Q, workspace, O, LSE, stream=None):
+    """Attention of one query [B, H, d] for each sequence over the keys paged_topk selected."""
+    _here(Q, workspace, O, LSE)
+    _shaped("Q", Q, (p.B, p.H, p.d), p)
+    _shaped("O", O, (p.B, p.H, p.d), p)
+    _shaped("LSE", LSE, (p.B, p.H))
+    check("dma_paged_attn", load().dma_paged_attn(ctypes.byref(p), ctypes.byref(c), _ptr(Q), _ptr(workspace),
+                                                  _nbytes(workspace), _ptr(O), _ptr(LSE), _stream(stream)))
+
+
 # ---------------------------------------------------------------- convenience (torch allocation)
+
+def alloc_paged_workspace(p, c, device="cuda"):
+    """A workspace for the paged calls (torch allocation, status word cleared)."""
+    import torch
+    return torch.zeros(paged_layout(p, c).bytes, dtype=torch.uint8, device=device)
+
 
 def alloc_prep_workspace(p, r, device="cuda"):
     """A workspace for prep_bwd (torch allocation)."""

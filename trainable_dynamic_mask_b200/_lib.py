@@ -52,6 +52,16 @@ class DmaPrepStrides(ctypes.Structure):
     _fields_ = [("q", ctypes.c_int64 * 3), ("k", ctypes.c_int64 * 3), ("v", ctypes.c_int64 * 3)]
 
 
+class DmaPages(ctypes.Structure):
+    _fields_ = [("K", c_vp), ("V", c_vp), ("delta", c_vp), ("table", c_vp), ("lens", c_vp), ("n_pages", c_i32),
+                ("page", c_i32), ("max_pages", c_i32), ("prefix", c_i32)]
+
+
+class DmaPagedLayout(ctypes.Structure):
+    _fields_ = [("bytes", c_sz), ("off_status", c_sz), ("off_rows", c_sz), ("off_sel", c_sz), ("off_cand", c_sz),
+                ("sel_len", c_i32), ("cand_len", c_i32)]
+
+
 # name -> argtypes (every function returns dma_status_t as int32 unless listed in _RESTYPES)
 _SIGS = {
     "dma_status_string": [c_i32],
@@ -83,6 +93,12 @@ _SIGS = {
     "dma_prep_bwd": [ctypes.POINTER(DmaParams), ctypes.POINTER(DmaPrep), ctypes.POINTER(DmaPrepStrides),
                      ctypes.POINTER(DmaPrepStrides), c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
                      c_vp, c_sz, c_vp],
+    "dma_paged_layout": [ctypes.POINTER(DmaParams), ctypes.POINTER(DmaPages), ctypes.POINTER(DmaPagedLayout)],
+    "dma_paged_append": [ctypes.POINTER(DmaParams), ctypes.POINTER(DmaPages), ctypes.POINTER(DmaPrep),
+                         ctypes.POINTER(DmaPrepStrides), c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_sz,
+                         c_vp],
+    "dma_paged_topk": [ctypes.POINTER(DmaParams), ctypes.POINTER(DmaPages), c_vp, c_sz, c_vp],
+    "dma_paged_attn": [ctypes.POINTER(DmaParams), ctypes.POINTER(DmaPages), c_vp, c_vp, c_sz, c_vp, c_vp, c_vp],
 }
 _RESTYPES = {"dma_status_string": ctypes.c_char_p, "dma_abi_version": c_i32}
 

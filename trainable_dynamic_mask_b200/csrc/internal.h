@@ -120,6 +120,47 @@ bool check_strides(const int64_t (&st)[3], bool bf16);
 cudaError_t launch_prep_fwd(const PrepArgs& a, bool bf16, int d, cudaStream_t s);
 cudaError_t launch_prep_bwd(const PrepArgs& a, bool bf16, int d, float* dq_weight, float* dk_weight, cudaStream_t s);
 
+// ---------------------------------------------------------------- paged cache (paged*.cu)
+constexpr int kPagedErr = 0x10000000;   // status bit: a page number or a length out of range
+constexpr int kPagedSplit = 256;        // selected keys per CTA of the attention over one row's list
+
+// Resolved paged problem: what the kernels read, and the workspace plan.
+struct PagedPlan {
+  int B, H, Hkv, d, w, N, G;
+  float scale;
+  bool bf16, shared;        // shared: the prefix is selected from and attended to once for the batch
+  const int32_t* w_heads;
+  char* K;
+  char* V;
+  float* delta;
+  const int32_t* table;
+  const int32_t* lens;
+  int n_pages, page_shift, max_pages, prefix;
+  int sel_len;              // keys a row's list may hold
+  int cand_len;             // shared: candidates of the prefix per head, min(w, prefix)
+  int n_split;              // partial results of a row's list
+  int n_psplit;             // shared: partial results of the candidates
+  size_t off_status, off_rows, off_sel, off_cand;
+  size_t off_ent;           // int2 [B*H, sel_len]: {slot of the cache, delta bits} beside off_sel
+  size_t off_crow;          // int32 [H]: candidates of the head (-1: a bad page among the prefix's)
+  size_t off_cent;          // int2 [H, cand_len]: as off_ent, beside off_cand
+  size_t off_count;         // int32 [B*H]: partial results written; 0 before and after every attention call
+  size_t off_part;          // f32 [B*H][n_psplit + n_split][d + 2]: m, l, o
+  size_t bytes;
+};
+struct PagedAppendArgs {
+  dma_prep_t r;
+  dma_prep_strides_t st;
+  int T;
+  const int32_t* starts;
+  const void *q, *k, *v, *Delta;
+  const float* A;
+  void* Q;
+};
+cudaError_t launch_paged_append(const PagedPlan& P, const PagedAppendArgs& a, void* ws, cudaStream_t s);
+cudaError_t launch_paged_topk(const PagedPlan& P, void* ws, cudaStream_t s);
+cudaError_t launch_paged_attn(const PagedPlan& P, const void* Q, void* ws, void* O, float* LSE, cudaStream_t s);
+
 // ---------------------------------------------------------------- launchers (cudaError_t)
 cudaError_t launch_gate_fwd(const Plan& P, const void* V, const void* Delta, const float* A,
                             float* delta, float* x_save, cudaStream_t s);

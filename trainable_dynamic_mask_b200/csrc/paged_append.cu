@@ -1,0 +1,338 @@
+// Appending tokens to the paged cache: keys normed and rotated into their slots, values copied, gate
+// values delta = exp(A softplus(v Delta)) formed from the values on the way, queries of the same tokens
+// normed and rotated.
+//
+// Two kernels that run side by side: the gate's product (the values of 16 tokens against Delta, tensor
+// cores for bf16) and the rows (a warp per token, as in prep.cu).  The second is launched as a
+// programmatic dependent of the first, which lets it go at once; it waits for the first only before it
+// ends, so that whatever follows in the stream finds both done.
+#include "rows.cuh"
+
+namespace dma {
+namespace {
+
+DMA_DEVINL float softplus_of(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
+
+// Where token t goes.
+struct Place {
+  int seq, pos;    // pos < 0: nothing of this token is written
+  int page, slot;
+};
+
+// Sequence and slot of token t; every lane of the warp calls it with the same t < T.
+DMA_DEVINL Place place_of(const PagedPlan& P, const PagedAppendArgs& a, int t, int32_t* status) {
+  const int lane = threadIdx.x & 31;
+  int seq = t, first = t, n = 1;
+  if (a.starts != nullptr) {
+    // number of sequences that end at or before t
+    seq = 0;
+    for (int i0 = 1; i0 <= P.B; i0 += 32) {
+      const int i = i0 + lane;
+      const bool before = i <= P.B && __ldg(a.starts + i) <= t;
+      seq += __popc(__ballot_sync(0xffffffffu, before));
+    }
+    if (seq >= P.B) return {0, -1, 0, 0};   // padding behind the last sequence
+    first = __ldg(a.starts + seq);
+    n = __ldg(a.starts + seq + 1) - first;
+    if (t < first) return {0, -1, 0, 0};    // padding in front of the first one
+  }
+  const int len = __ldg(P.lens + seq);
+  if (len <= 0) return {seq, -1, 0, 0};
+  const int pos = len - n + (t - first);
+  int page = -1;
+  if (pos >= 0 && pos < len && len <= P.N) page = __ldg(P.table + (size_t)seq * P.max_pages + (pos >> P.page_shift));
+  if (page < 0 || page >= P.n_pages) {
+    if (lane == 0) atomicOr(status, kPagedErr);
+    return {seq, -1, 0, 0};
+  }
+  return {seq, pos, page, pos & ((1 << P.page_shift) - 1)};
+}
+
+// ---------------------------------------------------------------- rows
+
+constexpr int kArThreads = 256;
+constexpr int kArWarps = kArThreads / 32;
+
+template <typename T, int D, int U>
+__global__ void __launch_bounds__(kArThreads)
+paged_rows_kernel(PagedPlan P, PagedAppendArgs a, int wt, int32_t* status) {
+  constexpr int L = D / 8, RPW = 32 / L;
+  __shared__ float2 tab[kArWarps][D / 2];
+  __shared__ Place place[kArWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tpb = kArWarps / wt, half = a.r.rot >> 1;
+  const int t0 = blockIdx.x * tpb;
+  if (warp < tpb) {
+    Place pl = {0, -1, 0, 0};
+    if (t0 + warp < a.T) pl = place_of(P, a, t0 + warp, status);
+    if (lane == 0) place[warp] = pl;
+    if (pl.pos >= 0)
+      for (int k = lane; k < half; k += 32) tab[warp][k] = turn_of(pl.pos, __ldg(a.r.inv_freq + k));
+  }
+  __syncthreads();
+  const Place pl = place[warp / wt];
+  if (pl.pos >= 0) {
+    const long long t = t0 + warp / wt;
+    const int grp = lane / L, e = (lane % L) * 8, page = 1 << P.page_shift;
+    LaneTurn turn;
+    lane_turn<L>(turn, tab[warp / wt], a.r.rot, a.r.interleaved != 0, lane);
+    const size_t slot = ((size_t)pl.page * P.Hkv * page + pl.slot) * D + e;   // of head 0
+#pragma unroll
+    for (int part = 0; part < 3; ++part) {   // keys, values, queries
+      if (part == 2 && a.q == nullptr) continue;
+      const int heads = part == 2 ? P.H : P.Hkv;
+      const int64_t* st = part == 0 ? a.st.k : part == 1 ? a.st.v : a.st.q;
+      const T* src = (const T*)(part == 0 ? a.k : part == 1 ? a.v : a.q) + t * st[1] + e;
+      T* dst = part == 0 ? (T*)P.K + slot : part == 1 ? (T*)P.V + slot : (T*)a.Q + (size_t)t * P.H * D + e;
+      const size_t dh = part == 2 ? (size_t)D : (size_t)page * D;
+      const long long sh = st[2];
+      const T* wp = (const T*)(part == 0 ? a.r.k_weight : part == 2 ? a.r.q_weight : nullptr);
+      float g[8];
+      if (wp) widen8(load_raw8(wp + e), g);
+      for (int h0 = (warp % wt) * RPW * U; h0 < heads; h0 += wt * RPW * U) {
+        Raw8<T> raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) raw[u] = load_raw8(src + min(h0 + u * RPW + grp, heads - 1) * sh);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int h = h0 + u * RPW + grp;
+          if (part == 1) {
+            if (h < heads) store_raw8(dst + h * dh, raw[u]);
+            continue;
+          }
+          float y[8];
+          widen8(raw[u], y);
+          if (wp) {
+            float ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
+            const float r = rsqrtf(row_sum<L>(ss) * (1.f / D) + a.r.eps);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] *= r * g[i];
+          }
+          rotate8<false>(y, turn, a.r.interleaved != 0);
+          if (h < heads) store8(dst + h * dh, y);
+        }
+      }
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the gate kernel in front is done too
+}
+
+// ---------------------------------------------------------------- gate, tensor cores
+
+constexpr int kAgTok = 16;        // tokens of a CTA: one m16 tile
+constexpr int kAgThreads = 256;
+constexpr int kAgWarps = kAgThreads / 32;
+
+// Offset of (token's page, head 0, slot) in the delta pages of the CTA's tokens; -1: none.
+DMA_DEVINL void gate_places(const PagedPlan& P, const PagedAppendArgs& a, int t0, int n, long long* where,
+                            int32_t* status) {
+  for (int i = threadIdx.x >> 5; i < n; i += kAgWarps) {
+    Place pl = {0, -1, 0, 0};
+    if (t0 + i < a.T) pl = place_of(P, a, t0 + i, status);
+    if ((threadIdx.x & 31) == 0)
+      where[i] = pl.pos < 0 ? -1 : ((long long)pl.page * P.H << P.page_shift) + pl.slot;
+  }
+}
+
+// x [16 tokens, H] = v [16, K] Delta [K, H], K = Hkv d: the warps split K in steps of 16 and their tiles
+// are summed through shared memory (in a fixed order).  bf16 products are exact in float32, in which all
+// is accumulated.  Everything the CTA reads is in flight before the first wait: one trip to memory is
+// what bounds a decode step.
+template <int HT>   // column tiles of 8 heads
+__global__ void __launch_bounds__(kAgThreads)
+paged_gate_mma_kernel(PagedPlan P, PagedAppendArgs a, int32_t* status) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  extern __shared__ __align__(128) unsigned char sm[];
+  __shared__ long long where[kAgTok];
+  const int K = P.Hkv * P.d, KC = K / 8, dch = P.d / 8;
+  uint16_t* Vs = reinterpret_cast<uint16_t*>(sm);                   // [16][K], chunk c of row r at c ^ (r & 7)
+  uint16_t* Ds = Vs + kAgTok * K;                                   // [K][8 HT]
+  float* red = reinterpret_cast<float*>(Ds + (size_t)K * 8 * HT);   // [8 warps][16][8 HT]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int t0 = blockIdx.x * kAgTok;
+  const uint16_t* v = static_cast<const uint16_t*>(a.v);
+  const uint16_t* Delta = static_cast<const uint16_t*>(a.Delta);
+  for (int u = tid; u < kAgTok * KC; u += kAgThreads) {
+    const int r = u / KC, kc = u % KC, g = kc / dch, c = kc % dch;
+    const bool in = t0 + r < a.T;
+    const uint16_t* src = in ? v + (long long)(t0 + r) * a.st.v[1] + g * a.st.v[2] + c * 8 : v;
+    cp_async_16(smem_u32(Vs + (size_t)r * K + ((kc ^ (r & 7)) * 8)), src, in ? 16 : 0);
+  }
+  if ((P.H & 7) == 0) {
+    const int hc = P.H / 8;
+    for (int u = tid; u < K * HT; u += kAgThreads) {
+      const int r = u / HT, c = u % HT;
+      const bool in = c < hc;
+      cp_async_16(smem_u32(Ds + (size_t)r * 8 * HT + c * 8), in ? Delta + (size_t)r * P.H + c * 8 : Delta, in ? 16 : 0);
+    }
+  } else {
+    for (int u = tid; u < K * 8 * HT; u += kAgThreads) {
+      const int r = u / (8 * HT), h = u % (8 * HT);
+      Ds[u] = h < P.H ? Delta[(size_t)r * P.H + h] : (uint16_t)0;
+    }
+  }
+  cp_async_commit();
+  gate_places(P, a, t0, kAgTok, where, status);
+  cp_async_wait<0>();
+  __syncthreads();
+  float acc[HT][4];
+#pragma unroll
+  for (int n = 0; n < HT; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+  const uint32_t vs = smem_u32(Vs), ds = smem_u32(Ds);
+  const int arow = lane & 15, achunk = lane >> 4;
+  const int brow = lane & 15, btile = lane >> 4;
+  for (int ks = warp; ks < K / 16; ks += kAgWarps) {
+    uint32_t f[4];
+    const int kc = ks * 2 + achunk;
+    ldmatrix_x4(vs + (uint32_t)(arow * K + ((kc ^ (arow & 7)) * 8)) * 2, f[0], f[1], f[2], f[3]);
+#pragma unroll
+    for (int n = 0; n < HT; n += 2) {
+      uint32_t b0, b1, b2, b3;
+      ldmatrix_x4_trans(ds + (uint32_t)((ks * 16 + brow) * 8 * HT + (n + btile) * 8) * 2, b0, b1, b2, b3);
+      mma_bf16_16816(acc[n], f, b0, b1);
+      mma_bf16_16816(acc[n + 1], f, b2, b3);
+    }
+  }
+  const int g = lane >> 2, q = lane & 3;
+#pragma unroll
+  for (int n = 0; n < HT; ++n) {
+    float* w = red + (size_t)warp * kAgTok * 8 * HT + n * 8 + 2 * q;
+    *reinterpret_cast<float2*>(w + g * 8 * HT) = make_float2(acc[n][0], acc[n][1]);
+    *reinterpret_cast<float2*>(w + (g + 8) * 8 * HT) = make_float2(acc[n][2], acc[n][3]);
+  }
+  __syncthreads();
+  // consecutive threads take consecutive tokens of a head: neighbouring slots of one page
+  for (int o = tid; o < kAgTok * P.H; o += kAgThreads) {
+    const int t = o % kAgTok, h = o / kAgTok;
+    const long long at = where[t];
+    if (at < 0) continue;
+    float x = 0.f;
+#pragma unroll
+    for (int w = 0; w < kAgWarps; ++w) x += red[((size_t)w * kAgTok + t) * 8 * HT + h];
+    P.delta[at + ((long long)h << P.page_shift)] = expf(a.A[h] * softplus_of(x));
+  }
+}
+
+// ---------------------------------------------------------------- gate, any type and width
+
+constexpr int kAfTok = 8;      // tokens of a CTA
+constexpr int kAfK = 512;      // channels staged at a time
+
+// float32 storage (and bf16 rows too wide for the kernel above): the same product on the FMA pipe.
+// Thread = one head and one of NS slices of the staged channels, for 8 tokens.
+template <typename T>
+__global__ void __launch_bounds__(kAgThreads)
+paged_gate_kernel(PagedPlan P, PagedAppendArgs a, int HP, int32_t* status) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  extern __shared__ __align__(16) float fsm[];
+  __shared__ long long where[kAfTok];
+  float* Vs = fsm;                   // [kAfK][kAfTok]
+  float* red = Vs + kAfK * kAfTok;   // [NS][kAfTok][HP]
+  const int K = P.Hkv * P.d, NS = kAgThreads / HP;
+  const int tid = threadIdx.x, h = tid % HP, sl = tid / HP;
+  const int t0 = blockIdx.x * kAfTok;
+  const T* v = static_cast<const T*>(a.v);
+  const T* Delta = static_cast<const T*>(a.Delta);
+  gate_places(P, a, t0, kAfTok, where, status);
+  float acc[kAfTok];
+#pragma unroll
+  for (int i = 0; i < kAfTok; ++i) acc[i] = 0.f;
+  for (int k0 = 0; k0 < K; k0 += kAfK) {
+    const int kn = min(kAfK, K - k0);
+    __syncthreads();
+    for (int u = tid; u < kn * kAfTok; u += kAgThreads) {
+      const int t = u / kn, kk = u % kn, g = (k0 + kk) / P.d, c = (k0 + kk) % P.d;
+      Vs[kk * kAfTok + t] =
+          t0 + t < a.T ? load_as_f32(v + (long long)(t0 + t) * a.st.v[1] + g * a.st.v[2] + c) : 0.f;
+    }
+    __syncthreads();
+    if (h < P.H && sl < NS) {
+#pragma unroll 4
+      for (int kk = sl; kk < kn; kk += NS) {
+        const float dl = load_as_f32(Delta + (size_t)(k0 + kk) * P.H + h);
+        const float4 v0 = reinterpret_cast<const float4*>(Vs + kk * kAfTok)[0];
+        const float4 v1 = reinterpret_cast<const float4*>(Vs + kk * kAfTok)[1];
+        acc[0] = fmaf(v0.x, dl, acc[0]); acc[1] = fmaf(v0.y, dl, acc[1]);
+        acc[2] = fmaf(v0.z, dl, acc[2]); acc[3] = fmaf(v0.w, dl, acc[3]);
+        acc[4] = fmaf(v1.x, dl, acc[4]); acc[5] = fmaf(v1.y, dl, acc[5]);
+        acc[6] = fmaf(v1.z, dl, acc[6]); acc[7] = fmaf(v1.w, dl, acc[7]);
+      }
+    }
+  }
+  if (h < P.H && sl < NS) {
+#pragma unroll
+    for (int i = 0; i < kAfTok; ++i) red[(sl * kAfTok + i) * HP + h] = acc[i];
+  }
+  __syncthreads();
+  for (int o = tid; o < kAfTok * P.H; o += kAgThreads) {
+    const int t = o % kAfTok, hh = o / kAfTok;
+    const long long at = where[t];
+    if (at < 0) continue;
+    float x = 0.f;
+    for (int s = 0; s < NS; ++s) x += red[(s * kAfTok + t) * HP + hh];
+    P.delta[at + ((long long)hh << P.page_shift)] = expf(a.A[hh] * softplus_of(x));
+  }
+}
+
+template <int HT>
+cudaError_t launch_gate_mma(const PagedPlan& P, const PagedAppendArgs& a, size_t smem, int32_t* status, cudaStream_t s) {
+  const cudaError_t e = ensure_smem_limit(paged_gate_mma_kernel<HT>, (int)smem);
+  if (e != cudaSuccess) return e;
+  paged_gate_mma_kernel<HT><<<(a.T + kAgTok - 1) / kAgTok, kAgThreads, smem, s>>>(P, a, status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_gate(const PagedPlan& P, const PagedAppendArgs& a, int32_t* status, cudaStream_t s) {
+  const size_t K = (size_t)P.Hkv * P.d;
+  if (P.bf16) {
+    const int HT = P.H <= 16 ? 2 : P.H <= 32 ? 4 : 8;
+    const size_t smem = kAgTok * K * 2 + K * 8 * HT * 2 + (size_t)kAgWarps * kAgTok * 8 * HT * 4;
+    if (smem <= 200 * 1024)   // else the rows do not fit (more than about 2700 channels at 32 heads)
+      return HT == 2   ? launch_gate_mma<2>(P, a, smem, status, s)
+             : HT == 4 ? launch_gate_mma<4>(P, a, smem, status, s)
+                       : launch_gate_mma<8>(P, a, smem, status, s);
+  }
+  const int HP = P.H <= 16 ? 16 : P.H <= 32 ? 32 : 64;
+  const int smem = (kAfK * kAfTok + kAgThreads * kAfTok) * (int)sizeof(float);
+  const int blocks = (a.T + kAfTok - 1) / kAfTok;
+  if (P.bf16)
+    paged_gate_kernel<uint16_t><<<blocks, kAgThreads, smem, s>>>(P, a, HP, status);
+  else
+    paged_gate_kernel<float><<<blocks, kAgThreads, smem, s>>>(P, a, HP, status);
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_rows(const PagedPlan& P, const PagedAppendArgs& a, int32_t* status, cudaStream_t s) {
+  const int sms = sm_count();
+  int wt = 1;   // warps that share a token: enough to give every SM a block
+  while (wt < kArWarps && (long long)a.T * wt < (long long)sms * kArWarps) wt *= 2;
+  const int tpb = kArWarps / wt;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((a.T + tpb - 1) / tpb);
+  cfg.blockDim = dim3(kArThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_rows_kernel<T, D, 4>, P, a, wt, status);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const PagedPlan& P, const PagedAppendArgs& a, void* ws, cudaStream_t s) {
+  int32_t* status = ws_ptr<int32_t>(ws, P.off_status);
+  const cudaError_t e = launch_gate(P, a, status, s);
+  if (e != cudaSuccess) return e;
+  if (P.bf16)
+    return P.d == 128 ? launch_rows<uint16_t, 128>(P, a, status, s) : launch_rows<uint16_t, 64>(P, a, status, s);
+  return P.d == 128 ? launch_rows<float, 128>(P, a, status, s) : launch_rows<float, 64>(P, a, status, s);
+}
+
+}  // namespace dma
