@@ -203,6 +203,82 @@ def test_selection_and_attention(name):
     c.check(Q2, O2, L2)
 
 
+PREFIXED = {
+    # lens, prefix, H, Hkv, d, page, dtype, w, further arguments
+    "two": ([64, 65], 64, 2, 1, 64, 16, "bf16", 16, {}),
+    "few": ([320, 333, 0, 500, 320], 320, 4, 2, 128, 64, "bf16", 100, {}),
+    "wide": ([48 + 7 * i for i in range(19)], 48, 3, 3, 64, 16, "bf16", 64, {}),
+    "window_over_prefix": ([128, 1000, 200], 128, 2, 1, 128, 128, "bf16", 300, {}),
+    "ties": ([256 + 50 * i for i in range(33)], 256, 2, 1, 64, 32, "bf16", 90, dict(delta="levels")),
+    "constant": ([160, 170, 480], 160, 1, 1, 64, 32, "bf16", 80, dict(delta="constant")),
+    "heads": ([512, 700, 513], 512, 4, 2, 64, 16, "bf16", 200, dict(w_heads=[200, 1, 0, 999])),
+    "batch": ([4096 + i for i in range(70)], 4096, 4, 2, 128, 64, "bf16", 600, {}),
+    "long": ([40960, 50001], 40960, 2, 1, 128, 64, "bf16", 2048, {}),
+    "idle_first": ([0, 100, 96], 96, 2, 2, 64, 32, "bf16", 40, {}),
+    "float": ([64, 100, 90], 64, 2, 1, 64, 16, "f32", 30, {}),
+    "alone": ([90], 64, 2, 1, 64, 16, "bf16", 30, {}),
+}
+
+
+@pytest.mark.parametrize("name", PREFIXED)
+def test_shared_prefix(name):
+    lens, prefix, H, Hkv, d, page, dtype, w, more = PREFIXED[name]
+    c = Cache(lens, H, Hkv, d, page, dtype, w, seed=len(name), prefix=prefix, **more)
+    lay = c.dma.paged_layout(c.p, c.c)
+    assert (lay.cand_len > 0) == (dtype == "bf16" and len(lens) > 1)
+    out = c.run()
+    c.torch.cuda.synchronize()
+    c.check_selection()
+    c.check(*out)
+    again = c.run(out[0])
+    for x, y in zip(out, again):
+        assert c.torch.equal(x, y)
+
+
+def test_shared_prefix_masked_places_may_hold_anything():
+    """Candidates that one sequence selects and another does not hold infinities: only the first sees them."""
+    c = Cache([192, 320, 200], 2, 1, 64, 32, "bf16", 32, seed=3, prefix=192)
+    torch = c.torch
+    c.delta[c.table[1, 6:].long()] = 2.0 + torch.arange(32, device="cuda") / 64   # sequence 1 selects none of the prefix
+    Q, O, L = c.run()
+    assert all((x < 192).all() for x in c.selected()[0]) and all((x >= 192).all() for x in c.selected()[1])
+    for s in range(3):
+        c.K[c.table[s, :6].long()] = float("nan")
+        c.V[c.table[s, :6].long()] = -float("inf")
+    _, O2, L2 = c.run(Q)
+    assert torch.equal(O[1], O2[1]) and torch.equal(L[1], L2[1])
+    assert torch.isnan(O2[0].float()).all() and torch.isnan(L2[0]).all()
+    # an infinite value among finite keys reaches those who selected it, and no other channel
+    c = Cache([192, 320, 200], 1, 1, 64, 32, "bf16", 32, seed=3, prefix=192)
+    c.delta[c.table[1, 6:].long()] = 2.0 + torch.arange(32, device="cuda") / 64
+    want = c.run()
+    j = int(c.selected()[0][0][-1])
+    assert j in c.selected()[2][0]
+    c.V[c.table[0, j // 32].long(), 0, j % 32, 5] = float("inf")
+    got = c.run(want[0])
+    for s in (0, 2):
+        assert got[1][s, 0, 5] == float("inf")
+        other = torch.arange(64, device="cuda") != 5
+        assert (got[1][s, 0, other].float() - want[1][s, 0, other].float()).abs().max() <= 2.0 ** -8 * 4
+    assert torch.equal(got[1][1], want[1][1]) and torch.equal(got[2], want[2])
+
+
+def test_shared_prefix_bad_pages_and_short_lengths():
+    c = Cache([64, 100, 80], 2, 1, 64, 16, "bf16", 20, seed=4, prefix=64)
+    dma = c.dma
+    c.lens[2] = 63                       # shorter than the prefix it is said to share
+    Q, O, L = c.run()
+    assert dma.check_device_status(c.p, c.ws) == 0x10000000
+    assert (O[2] == 0).all() and (L[2] == -float("inf")).all()
+    dma.clear_device_status(c.p, c.ws)
+    c.lens_host = [64, 100, 0]
+    c.check(Q, O, L)
+    c.table[0, 1] = -7                   # sequence 0's row names the prefix
+    _, O, L = c.run(Q)
+    assert dma.check_device_status(c.p, c.ws) == 0x10000000
+    assert (O == 0).all() and (L == -float("inf")).all()
+
+
 def test_selection_longer_than_a_cluster_holds():
     # 8 x 49152 values stay on chip; the rest of the row is read again in every round
     c = Cache([500_003], 1, 1, 64, 64, "bf16", 5000, delta="bits")

@@ -140,6 +140,7 @@ struct PagedPlan {
   int cand_len;             // shared: candidates of the prefix per head, min(w, prefix)
   int n_split;              // partial results of a row's list
   int n_psplit;             // shared: partial results of the candidates
+  int cand_split;           // shared: candidates of a CTA (64, 128 or 256)
   size_t off_status, off_rows, off_sel, off_cand;
   size_t off_ent;           // int2 [B*H, sel_len]: {slot of the cache, delta bits} beside off_sel
   size_t off_crow;          // int32 [H]: candidates of the head (-1: a bad page among the prefix's)

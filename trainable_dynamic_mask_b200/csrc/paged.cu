@@ -35,13 +35,18 @@ dma_status_t paged_plan(const dma_params_t* p, const dma_pages_t* c, PagedPlan* 
   P->prefix = c->prefix;
   while ((1 << P->page_shift) < c->page) ++P->page_shift;
   // the candidates are multiplied with all sequences' queries on the tensor cores, in bf16
-  P->shared = false;
+  P->shared = c->prefix > 0 && P->bf16 && P->B > 1;
   const int rest = P->shared ? P->N - P->prefix : P->N;
   P->sel_len = P->w < rest ? P->w : rest;
   if (P->sel_len < 1) P->sel_len = 1;
   P->cand_len = P->shared ? (P->w < P->prefix ? P->w : P->prefix) : 0;
   P->n_split = (P->sel_len + kPagedSplit - 1) / kPagedSplit;
-  P->n_psplit = (P->cand_len + kPagedSplit - 1) / kPagedSplit;
+  // candidates of a CTA: 256, or as few as 64 where that leaves SMs without one (a fixed count of 148
+  // keeps the workspace's plan independent of the device)
+  P->cand_split = 256;
+  const int64_t tiles = (int64_t)P->H * ((P->B + 63) / 64);
+  while (P->cand_split > 64 && tiles * ((P->cand_len + P->cand_split - 1) / P->cand_split) < 148) P->cand_split /= 2;
+  P->n_psplit = (P->cand_len + P->cand_split - 1) / P->cand_split;
   const size_t BH = (size_t)P->B * P->H;
   size_t off = 0;
   auto take = [&](size_t bytes) {

@@ -166,6 +166,270 @@ paged_list_kernel(const T* __restrict__ Q, const T* __restrict__ K, const T* __r
   join_row<T, D>(prow, n_psplit + n_act, O + (size_t)row * D, LSE + row);
 }
 
+// ---------------------------------------------------------------- shared prefix
+
+constexpr int kPcThreads = 128;
+constexpr int kPcTile = 64;    // candidates of a pipeline stage
+constexpr int kPcMost = 256;   // candidates of a CTA at most
+
+template <int D> constexpr int cand_smem() { return (64 + 4 * kPcTile) * D * 2; }   // Q, 2 x (K, V)
+
+// CTA = (part of a head's candidates, head, 16 R sequences).  Four warps: R groups of 16 sequences times
+// 4 / R groups of keys, so that a small batch still uses them all.  Tiles of 64 candidates' K and V rows
+// are gathered with 16-byte asynchronous copies (swizzled by row, conflict-free for ldmatrix), one tile
+// ahead.  A weight is split into two bf16 parts, both multiplied with V: one part alone would round every
+// weight to 8 bits, as much as the output's own rounding.
+// A candidate that a sequence did not select has weight exactly 0 there; if its V row holds an infinity or
+// NaN, 0 times that would still spoil the sum, so a tile with such a value is added up in plain
+// arithmetic that leaves weights of 0 out.
+template <int D, int R>
+__global__ void __launch_bounds__(kPcThreads)
+paged_cand_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ K, const uint16_t* __restrict__ V,
+                  const int4* __restrict__ rows, const int32_t* __restrict__ crow, const int2* __restrict__ cent,
+                  float* __restrict__ part, int B, int H, int Hkv, int page_shift, int cand_len, int cand_split,
+                  int n_part, float scale) {
+  constexpr int CH = D / 8, KG = 4 / R, NT = 8 / KG, NO = D / 8;   // NT, NO: 8-wide tiles of keys, channels
+  extern __shared__ __align__(128) unsigned char csm[];
+  uint16_t* Qs = reinterpret_cast<uint16_t*>(csm);   // [16 R][D]
+  uint16_t* Ks = Qs + 64 * D;                        // [2][64][D]
+  uint16_t* Vs = Ks + 2 * kPcTile * D;               // [2][64][D]
+  __shared__ uint32_t ckey[kPcMost];
+  __shared__ float cdel[kPcMost];
+  __shared__ int cslot[kPcMost];
+  __shared__ float gm[4][16], gl[4][16];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = blockIdx.y, g = h / (H / Hkv), s0 = blockIdx.z * 16 * R;
+  const int rg = warp / KG, kg = warp % KG;
+  const int c0 = blockIdx.x * cand_split;
+  const int nc = max(0, min(crow[h], min(cand_len, c0 + cand_split)) - c0);
+  const int nt = (nc + kPcTile - 1) / kPcTile;
+  for (int i = tid; i < nt * kPcTile; i += kPcThreads) {
+    int2 e = make_int2(0, 0);
+    if (i < nc) e = cent[(size_t)h * cand_len + c0 + i];
+    cslot[i] = e.x;
+    cdel[i] = __int_as_float(e.y);
+    ckey[i] = i < nc ? order_key(__int_as_float(e.y)) : 0u;
+  }
+  for (int u = tid; u < 16 * R * CH; u += kPcThreads) {
+    const int r = u / CH, c = u % CH;
+    const bool in = s0 + r < B;
+    cp_async_16(smem_u32(Qs) + swz(r, c, CH), Q + ((size_t)(in ? s0 + r : 0) * H + h) * D + c * 8, in ? 16 : 0);
+  }
+  __syncthreads();
+  const int mask = (1 << page_shift) - 1;
+  auto load_tile = [&](int t) {
+    const uint32_t kd = smem_u32(Ks + (t & 1) * kPcTile * D), vd = smem_u32(Vs + (t & 1) * kPcTile * D);
+#pragma unroll
+    for (int i = 0; i < kPcTile * CH / kPcThreads; ++i) {
+      const int u = tid + i * kPcThreads, r = u / CH, c = u % CH, j = t * kPcTile + r, slot = cslot[j];
+      const size_t at = ((((size_t)(slot >> page_shift) * Hkv + g) << page_shift) + (slot & mask)) * D + c * 8;
+      const int n = j < nc ? 16 : 0;
+      cp_async_16(kd + swz(r, c, CH), K + at, n);
+      cp_async_16(vd + swz(r, c, CH), V + at, n);
+    }
+  };
+  if (nt > 0) load_tile(0);
+  cp_async_commit();
+  // this lane's two sequences, s0 + 16 rg + lane / 4 and 8 behind it: their edges
+  uint32_t edge[2];
+  int cut[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int s = s0 + rg * 16 + (lane >> 2) + r * 8;
+    edge[r] = 0xffffffffu;
+    cut[r] = 0;
+    if (s < B) {
+      const int4 rec = rows[(size_t)s * H + h];
+      edge[r] = (uint32_t)rec.y;
+      cut[r] = rec.z;
+    }
+  }
+  float o[NO][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+  for (int n = 0; n < NO; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
+  uint32_t qf[D / 16][4];
+  for (int t = 0; t < nt; ++t) {
+    if (t + 1 < nt) load_tile(t + 1);
+    cp_async_commit();
+    cp_async_wait<1>();
+    __syncthreads();
+    if (t == 0) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        ldmatrix_x4(smem_u32(Qs) + swz(rg * 16 + (lane & 15), 2 * k + (lane >> 4), CH), qf[k][0], qf[k][1], qf[k][2],
+                    qf[k][3]);
+    }
+    const uint32_t kb = smem_u32(Ks + (t & 1) * kPcTile * D), vb = smem_u32(Vs + (t & 1) * kPcTile * D);
+    // an exponent of all ones anywhere in the V tile
+    uint32_t odd = 0u;
+    {
+      const uint4* vp = reinterpret_cast<const uint4*>(Vs + (t & 1) * kPcTile * D);
+#pragma unroll
+      for (int i = 0; i < kPcTile * CH / kPcThreads; ++i) {
+        const uint4 w = vp[tid + i * kPcThreads];
+        odd |= ((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) |
+               ((w.z & 0x7f807f80u) + 0x00800080u) | ((w.w & 0x7f807f80u) + 0x00800080u);
+      }
+    }
+    const bool plain = __syncthreads_or((odd & 0x80008000u) != 0u);
+    const int key0 = kg * (kPcTile / KG);   // this warp's keys of the tile
+    float x[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[n][i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+      for (int n = 0; n < NT; n += 2) {
+        uint32_t b0, b1, b2, b3;
+        ldmatrix_x4(kb + swz(key0 + n * 8 + (lane & 7) + (lane >> 4) * 8, 2 * k + ((lane >> 3) & 1), CH), b0, b1, b2, b3);
+        mma_bf16_16816(x[n], qf[k], b0, b1);
+        mma_bf16_16816(x[n + 1], qf[k], b2, b3);
+      }
+    float mx[2] = {m[0], m[1]};
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = t * kPcTile + key0 + n * 8 + 2 * (lane & 3) + (i & 1), r = i >> 1;
+        const uint32_t key = ckey[j];
+        const bool take = key > edge[r] || (key == edge[r] && key != 0u && c0 + j < cut[r]);
+        x[n][i] = take ? fmaf(x[n][i], scale, cdel[j]) : -INFINITY;
+        mx[r] = fmaxf(mx[r], x[n][i]);
+      }
+    float ref[2], keep[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+      mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+      ref[r] = mx[r] == -INFINITY ? 0.f : mx[r];
+      keep[r] = exp_diff(m[r], ref[r]);
+      m[r] = mx[r];
+      l[r] *= keep[r];
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[n][i] = exp_diff(x[n][i], ref[i >> 1]);
+        l[i >> 1] += x[n][i];
+      }
+#pragma unroll
+    for (int n = 0; n < NO; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[n][i] *= keep[i >> 1];
+    if (!plain) {
+#pragma unroll
+      for (int k = 0; k < NT / 2; ++k) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float p0 = x[2 * k + (i >> 1)][(i & 1) * 2], p1 = x[2 * k + (i >> 1)][(i & 1) * 2 + 1];
+          hi[i] = pack_bf16x2(p0, p1);
+          lo[i] = pack_bf16x2(p0 - __uint_as_float(hi[i] << 16), p1 - __uint_as_float(hi[i] & 0xffff0000u));
+        }
+#pragma unroll
+        for (int n = 0; n < NO; n += 2) {
+          uint32_t b0, b1, b2, b3;
+          ldmatrix_x4_trans(vb + swz(key0 + k * 16 + (lane & 15), n + (lane >> 4), CH), b0, b1, b2, b3);
+          mma_bf16_16816(o[n], hi, b0, b1);
+          mma_bf16_16816(o[n + 1], hi, b2, b3);
+          mma_bf16_16816(o[n], lo, b0, b1);
+          mma_bf16_16816(o[n + 1], lo, b2, b3);
+        }
+      }
+    } else {
+      const unsigned char* vrow = reinterpret_cast<const unsigned char*>(Vs + (t & 1) * kPcTile * D);
+#pragma unroll
+      for (int n8 = 0; n8 < NT; ++n8)
+#pragma unroll 1
+      for (int j8 = 0; j8 < 8; ++j8) {
+        // weights of key j: in register j % 2 of lane (j % 8) / 2 of each quad
+        const int j = n8 * 8 + j8, src = (lane & ~3) | (j8 >> 1);
+        const float p0 = __shfl_sync(0xffffffffu, (j8 & 1) ? x[n8][1] : x[n8][0], src);
+        const float p1 = __shfl_sync(0xffffffffu, (j8 & 1) ? x[n8][3] : x[n8][2], src);
+#pragma unroll
+        for (int n = 0; n < NO; ++n) {
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(vrow + swz(key0 + j, n, CH) + (lane & 3) * 4);
+          const float v0 = __uint_as_float(w << 16), v1 = __uint_as_float(w & 0xffff0000u);
+          if (p0 != 0.f) {
+            o[n][0] = fmaf(p0, v0, o[n][0]);
+            o[n][1] = fmaf(p0, v1, o[n][1]);
+          }
+          if (p1 != 0.f) {
+            o[n][2] = fmaf(p1, v0, o[n][2]);
+            o[n][3] = fmaf(p1, v1, o[n][3]);
+          }
+        }
+      }
+    }
+    __syncthreads();   // the tile's buffers may be filled again
+  }
+  cp_async_wait<0>();
+  __syncthreads();
+  // the warps' results side by side in the tiles' place, the key groups of a sequence joined
+  float* os = reinterpret_cast<float*>(Ks);   // [4 warps][16][D]
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    const int i = (lane >> 2) + r * 8;
+    if ((lane & 3) == 0) {
+      gm[warp][i] = m[r];
+      gl[warp][i] = l[r];
+    }
+#pragma unroll
+    for (int n = 0; n < NO; ++n)
+      *reinterpret_cast<float2*>(os + (warp * 16 + i) * D + n * 8 + 2 * (lane & 3)) =
+          make_float2(o[n][2 * r], o[n][2 * r + 1]);
+  }
+  __syncthreads();
+  for (int u = tid; u < 16 * R * (D / 4); u += kPcThreads) {
+    const int r = u / (D / 4), c = u % (D / 4) * 4, w0 = (r >> 4) * KG, i = r & 15;
+    if (s0 + r >= B) continue;
+    float M = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < KG; ++q) M = fmaxf(M, gm[w0 + q][i]);
+    const float ref = M == -INFINITY ? 0.f : M;
+    float sum = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int q = 0; q < KG; ++q) {
+      const float w = exp_diff(gm[w0 + q][i], ref);
+      const float4 v = *reinterpret_cast<const float4*>(os + ((w0 + q) * 16 + i) * D + c);
+      sum = fmaf(gl[w0 + q][i], w, sum);
+      a.x = fmaf(v.x, w, a.x); a.y = fmaf(v.y, w, a.y); a.z = fmaf(v.z, w, a.z); a.w = fmaf(v.w, w, a.w);
+    }
+    float* out = part + (((size_t)(s0 + r) * H + h) * n_part + blockIdx.x) * (D + 2);
+    if (c == 0) {
+      out[0] = M;
+      out[1] = sum;
+    }
+    out[2 + c] = a.x; out[3 + c] = a.y; out[4 + c] = a.z; out[5 + c] = a.w;
+  }
+}
+
+template <int D, int R>
+cudaError_t launch_cand(const PagedPlan& P, const void* Q, void* ws, cudaStream_t s) {
+  const cudaError_t e = ensure_smem_limit(paged_cand_kernel<D, R>, cand_smem<D>());
+  if (e != cudaSuccess) return e;
+  paged_cand_kernel<D, R><<<dim3(P.n_psplit, P.H, (P.B + 16 * R - 1) / (16 * R)), kPcThreads, cand_smem<D>(), s>>>(
+      (const uint16_t*)Q, (const uint16_t*)P.K, (const uint16_t*)P.V, ws_ptr<int4>(ws, P.off_rows),
+      ws_ptr<int32_t>(ws, P.off_crow), ws_ptr<int2>(ws, P.off_cent), ws_ptr<float>(ws, P.off_part), P.B, P.H, P.Hkv,
+      P.page_shift, P.cand_len, P.cand_split, P.n_psplit + P.n_split, P.scale);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_cand_rows(const PagedPlan& P, const void* Q, void* ws, cudaStream_t s) {
+  if (P.B <= 16) return launch_cand<D, 1>(P, Q, ws, s);
+  if (P.B <= 32) return launch_cand<D, 2>(P, Q, ws, s);
+  return launch_cand<D, 4>(P, Q, ws, s);
+}
+
 template <typename T, int D, int U>
 cudaError_t launch_list(const PagedPlan& P, const void* Q, void* ws, void* O, float* LSE, cudaStream_t s) {
   paged_list_kernel<T, D, U><<<dim3(P.n_split, P.B * P.H), kPlThreads, 0, s>>>(
@@ -178,6 +442,10 @@ cudaError_t launch_list(const PagedPlan& P, const void* Q, void* ws, void* O, fl
 }  // namespace
 
 cudaError_t launch_paged_attn(const PagedPlan& P, const void* Q, void* ws, void* O, float* LSE, cudaStream_t s) {
+  if (P.shared) {
+    const cudaError_t e = P.d == 128 ? launch_cand_rows<128>(P, Q, ws, s) : launch_cand_rows<64>(P, Q, ws, s);
+    if (e != cudaSuccess) return e;
+  }
   if (P.bf16)
     return P.d == 128 ? launch_list<uint16_t, 128, 8>(P, Q, ws, O, LSE, s)
                       : launch_list<uint16_t, 64, 8>(P, Q, ws, O, LSE, s);
