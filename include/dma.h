@@ -420,7 +420,8 @@ dma_status_t dma_prep_bwd(const dma_params_t* p, const dma_prep_t* r, const dma_
  *   K, V     [n_pages, Hkv, page, d] dtype;  delta [n_pages, H, page] float32
  *   table    int32 [B, max_pages];  lens int32 [B]: cache lengths, tokens being appended included.  A length
  *            of 0 (or below) is an idle row: nothing is appended, O = 0 and LSE = -inf.
- *   page     a power of two from 16 to 1024; n_pages * page < 2^31; N <= max_pages * page
+ *   page     a power of two from 16 to 1024; n_pages * page and n_pages * H < 2^31;
+ *            N <= max_pages * page
  *   prefix   0, or a multiple of page: the leading positions that every sequence shares: their table entries
  *            are those of sequence 0 (whose row holds them even if it is idle).  The selection and the
  *            attention over them are then computed once for the whole batch; the results are those of

@@ -182,6 +182,38 @@ CASES = {
     "long": ([70001, 65536], 2, 1, 64, 64, "bf16", 1000, {}),
 }
 
+# enough long rows for the selection that sieves: lengths that sieve at every group size and that do not,
+# values alike so that the sieve's list overflows, a few large values among many (a wide range of keys)
+SIEVED = {
+    "lengths": ([20000, 17001, 150, 8 * 150, 8 * 150 - 1, 2400, 4801, 0, 1, 19999, 12345, 16384], "gate"),
+    "ties": ([20000] * 6 + [19000 + i for i in range(6)], "levels"),
+    "constant": ([18000, 20000, 19001, 400] * 3, "constant"),
+    "any_bits": ([20000 - 117 * i for i in range(12)], "bits"),
+}
+
+
+@pytest.mark.parametrize("name", SIEVED)
+def test_selection_of_many_long_rows(name):
+    lens, kind = SIEVED[name]
+    c = Cache(lens, 16, 1, 64, 64, "bf16", 150, seed=31, delta=kind)
+    if kind == "gate":   # the best keys all in one place, as where a gate follows the content
+        c.delta[c.table[0, 100:103].long()] += 1.0
+    c.dma.paged_topk(c.p, c.c, c.ws)
+    c.torch.cuda.synchronize()
+    c.check_selection()
+    assert c.dma.check_device_status(c.p, c.ws) == 0
+
+
+def test_sieved_row_with_a_bad_page():
+    c = Cache([20000] * 12, 16, 1, 64, 64, "bf16", 150, seed=32)
+    c.table[3, 200] = -5
+    c.dma.paged_topk(c.p, c.c, c.ws)
+    assert c.dma.check_device_status(c.p, c.ws) == 0x10000000
+    got = c.selected()
+    assert all(got[3][h].size == 0 for h in range(16))
+    _, _, delta = c.row(4)
+    np.testing.assert_array_equal(got[4][0], c.chosen(delta[0], 0))
+
 
 @pytest.mark.parametrize("name", CASES)
 def test_selection_and_attention(name):

@@ -1,13 +1,20 @@
 // Top-w selection of every row (sequence, head) over the paged gate values.
 //
 // A row of n values is split over a cluster of C CTAs, each of which keeps its part in shared memory as
-// order keys: the values are read once.  The edge (the key of the last place) is found by counting, from
-// the row's smallest to its largest key, 2048 equal intervals at a time: the interval that holds the edge
-// is split again, so that three rounds settle any 32-bit keys and values that lie close together (gate
-// values do: exp of something near 0) still spread over all counters.  The counters of a cluster are
-// summed through distributed shared memory.  Then each warp counts the selected keys of its own stretch,
-// and writes them behind those of the stretches before it: the list comes out in ascending position, ties
-// to the lower position, without sorting.
+// order keys: the values are read once.  The edge (the key of the last place) is found by counting: the
+// interval from the row's smallest to its largest key is cut into 4 counters a thread (gate values lie
+// close together, so they spread over counters where fixed digits of the key would not), the counters of
+// the cluster are summed through distributed shared memory, and the keys of the counter that holds the
+// edge, a few dozen as a rule, are ranked against each other.  Where ties leave more of them than threads,
+// that counter's interval is cut again; four rounds settle any keys.  Then each warp counts the selected
+// keys of its own stretch, and writes them behind those of the stretches before it: the list comes out in
+// ascending position, ties to the lower position, without sorting.
+//
+// Long rows in large numbers (SIEVE) are not kept: the first reading only keeps the maxima of groups of 8
+// keys.  The w-th largest maximum is a lower bound of the edge, and with at least 2 w groups a close one:
+// only the groups that reach it are read again (from L2 by then), and little more than w keys are left for
+// the steps above.  All of that compares plain floats, and one key in 8 is counted: shared-memory atomics
+// are what counting costs.
 //
 // With a shared prefix the same kernel first selects the prefix's best w for each head (the candidates),
 // then takes each row's best w of (candidates, the row's own positions behind the prefix): the best of a
@@ -21,10 +28,9 @@ namespace cg = cooperative_groups;
 namespace dma {
 namespace {
 
-constexpr int kPsThreads = 512;
-constexpr int kPsWarps = kPsThreads / 32;
-constexpr int kPsBins = 2048;
 constexpr int kPsMaxCluster = 8;
+constexpr int kPsGroup = 8;           // sieve: keys of a maximum
+constexpr int kPsMaxBatches = 128;    // 128 groups that a warp reads again together
 
 enum SelMode { kRows, kCandidates, kRest };   // a whole row; the prefix, per head; candidates + the rest
 
@@ -32,21 +38,52 @@ enum SelMode { kRows, kCandidates, kRest };   // a whole row; the prefix, per he
 struct PsShared {
   uint32_t kmin, kmax;
   int valid, bad;
-  int4 count;   // keys above and at the edge among the candidates, above and at the edge behind them
+  int4 count;    // keys above and at the edge among the candidates, above and at the edge behind them
+  int members;   // keys in the interval being ranked
 };
 
-template <SelMode M>
-__global__ void __launch_bounds__(kPsThreads)
+// Sum of x over the warps before this one, and over all of them (NW <= 32 warps; x alike in a warp).
+template <int NW> DMA_DEVINL int2 warps_before(int x, int* buf) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) buf[warp] = x;
+  __syncthreads();
+  int v = lane < NW ? buf[lane] : 0;
+  const int own = v;
+#pragma unroll
+  for (int o = 1; o < NW; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  return make_int2(__shfl_sync(0xffffffffu, v - own, warp), __shfl_sync(0xffffffffu, v, NW - 1));
+}
+
+template <SelMode M, int NT, bool SIEVE>
+__global__ void __launch_bounds__(NT, NT == 512 ? 2 : 6)
 paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict__ sel, int2* __restrict__ ent,
                     int32_t* __restrict__ crow, int32_t* __restrict__ cand, int2* __restrict__ cent,
-                    int32_t* __restrict__ counters, int32_t* __restrict__ status, int cap) {
+                    int32_t* __restrict__ counters, int32_t* __restrict__ status, int cap, int page_cap,
+                    int list_cap) {
+  constexpr int NW = NT / 32, BINS = 4 * NT, LB = NT == 512 ? 11 : 9;
+  static_assert(BINS == 1 << LB, "four counters a thread");
+  static_assert(!SIEVE || M == kRows, "candidates and their rest are short or few");
   extern __shared__ __align__(16) uint32_t keys[];   // [cap] this CTA's stretch, as far as it fits
-  __shared__ __align__(16) int hist[2][kPsBins];
-  __shared__ PsShared sh;
-  __shared__ int wsum[kPsWarps][4];
-  __shared__ int found_bin, found_above;
+  int* pages = reinterpret_cast<int*>(keys + cap);   // [page_cap] the stretch's pages
+  __shared__ __align__(16) int hist[BINS];
+  __shared__ uint32_t list[NT], every[NT];
+  __shared__ __align__(16) int mhist[SIEVE ? BINS : 4];
+  __shared__ PsShared sh, msh;
+  __shared__ int2 batch[SIEVE ? kPsMaxBatches : 1];       // {first, number} in the list
+  __shared__ int2 batch_in[SIEVE ? kPsMaxBatches : 1];    // keys above and at the edge, then those in front
+  __shared__ int listed_total;
+  __shared__ int wbuf[5][NW];
+  __shared__ int found_bin, found_above, found_count;
+  __shared__ uint32_t found_key;
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  auto all_sync = [&]() {
+    if (C > 1) cl.sync();
+    else __syncthreads();
+  };
   const int row = blockIdx.y, h = M == kCandidates ? row : row % P.H, b = M == kCandidates ? 0 : row / P.H;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int W = row_window(P.w_heads, h, P.H, P.w);
@@ -68,93 +105,344 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
   const int seg = ((n + C - 1) / C + 3) & ~3;
   const int i0 = min(rank * seg, n), i1 = min(i0 + seg, n), ns = i1 - i0;
   const int2* ce = M == kRest ? cent + (size_t)h * P.cand_len : nullptr;
-
+  // what the steps after the first reading work on: the stretch (the first `res` keys resident, what lies
+  // behind them is read again in every round), or, sieved, a list of keys and their indices
+  int items = ns, res = min(ns, cap);
+  bool sieved = false;
+  const int tab0 = (base + max(i0 - n1p, 0)) >> P.page_shift;
+  const int np = i1 > n1p && i1 > i0 ? ((base + i1 - 1 - n1p) >> P.page_shift) - tab0 + 1 : 0;
+  for (int i = tid; i < min(np, page_cap); i += NT) {
+    int pg = __ldg(tab + tab0 + i);
+    if (pg < 0 || pg >= P.n_pages) {
+      bad = true;
+      pg = 0;
+    }
+    pages[i] = pg * P.H + h;
+  }
+  if (tid == 0) {
+    sh.kmin = 0xffffffffu;
+    sh.kmax = 0u;
+    sh.valid = 0;
+    sh.bad = 0;
+    sh.members = 0;
+    msh = sh;
+    listed_total = 0;
+  }
+  *reinterpret_cast<int4*>(hist + 4 * tid) = make_int4(0, 0, 0, 0);
+  if (SIEVE) *reinterpret_cast<int4*>(mhist + 4 * tid) = make_int4(0, 0, 0, 0);
+  __syncthreads();
+  // row of the delta pages (page number x H + h) that holds a position
+  auto page_row = [&](int pos) -> int {
+    const int i = (pos >> P.page_shift) - tab0;
+    if (i < page_cap) return pages[i];
+    int pg = __ldg(tab + tab0 + i);
+    if (pg < 0 || pg >= P.n_pages) {
+      bad = true;
+      pg = 0;
+    }
+    return pg * P.H + h;
+  };
+  auto slot_of = [&](int pos) -> int { return (page_row(pos) / P.H << P.page_shift) + (pos & (page - 1)); };
+  auto value4 = [&](int pos) -> float4 {
+    return *reinterpret_cast<const float4*>(P.delta + ((size_t)page_row(pos) << P.page_shift) + (pos & (page - 1)));
+  };
   // order keys of indices i .. i + 3 (i a multiple of 4); 0 where there is nothing
   auto load4 = [&](int i) -> uint4 {
     uint4 k = make_uint4(0u, 0u, 0u, 0u);
-    uint32_t* kk = &k.x;
     if (M == kRest && i < n1p) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (i + u < n1) kk[u] = order_key(__int_as_float(ce[i + u].y));
+      if (i < n1) k.x = order_key(__int_as_float(ce[i].y));
+      if (i + 1 < n1) k.y = order_key(__int_as_float(ce[i + 1].y));
+      if (i + 2 < n1) k.z = order_key(__int_as_float(ce[i + 2].y));
+      if (i + 3 < n1) k.w = order_key(__int_as_float(ce[i + 3].y));
       return k;
     }
     const int pos = base + i - n1p;
-    const int pg = __ldg(tab + (pos >> P.page_shift));
-    if (pg < 0 || pg >= P.n_pages) {
-      bad = true;
-      return k;
-    }
-    const float4 f = *reinterpret_cast<const float4*>(P.delta + (((size_t)pg * P.H + h) << P.page_shift) +
-                                                      (pos & (page - 1)));
+    const float4 f = value4(pos);
     k.x = order_key(f.x);
     if (i + 1 < n) k.y = order_key(f.y);
     if (i + 2 < n) k.z = order_key(f.z);
     if (i + 3 < n) k.w = order_key(f.w);
     return k;
   };
-  const int res = min(ns, cap);   // resident part; what lies behind it is read again in every round
-  auto key_at = [&](int i) -> uint32_t {
-    if (i < res) return keys[i];
-    const uint4 k = load4((i0 + i) & ~3);
-    const int u = (i0 + i) & 3;
-    return u == 0 ? k.x : u == 1 ? k.y : u == 2 ? k.z : k.w;
+  // four keys at local index i (a multiple of 4)
+  auto keys4 = [&](int i) -> uint4 {
+    return i < cap ? *reinterpret_cast<const uint4*>(keys + i) : load4(i0 + i);
+  };
+  // fn(key) for every key of the stretch, in no particular order
+  auto for_keys = [&](auto fn) {
+#pragma unroll 4
+    for (int i = tid * 4; i < res; i += NT * 4) {
+      const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
+      fn(k.x); fn(k.y); fn(k.z); fn(k.w);
+    }
+    for (int i = cap + tid * 4; i < items; i += NT * 4) {
+      const uint4 k = load4(i0 + i);
+      fn(k.x); fn(k.y); fn(k.z); fn(k.w);
+    }
   };
 
-  // ---- read the stretch once: keys, smallest, largest, how many
-  if (tid == 0) {
-    sh.kmin = 0xffffffffu;
-    sh.kmax = 0u;
-    sh.valid = 0;
-    sh.bad = 0;
-  }
-  __syncthreads();
+  // the counter (of 4 NT, summed over the cluster) that holds the want-th largest key, `above` keys lying
+  // above all of them: found_bin, found_above, found_count
+  auto find_bin = [&](int* counts, int above, int want, int* buf) {
+    // thread t sums counters 4 t' .. 4 t' + 3, t' = NT - 1 - t: from the top
+    const int b4 = (NT - 1 - tid) * 4;
+    int4 c = make_int4(0, 0, 0, 0);
+    {
+      int4 o[kPsMaxCluster];
+#pragma unroll
+      for (int r = 0; r < kPsMaxCluster; ++r)
+        o[r] = r < C ? *reinterpret_cast<const int4*>(cl.map_shared_rank(counts + b4, r)) : make_int4(0, 0, 0, 0);
+#pragma unroll
+      for (int r = 0; r < kPsMaxCluster; ++r) {
+        c.x += o[r].x; c.y += o[r].y; c.z += o[r].z; c.w += o[r].w;
+      }
+    }
+    const int mine = c.x + c.y + c.z + c.w;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const int excl = above + warps_before<NW>(__shfl_sync(0xffffffffu, incl, 31), buf).x + incl - mine;
+    if (excl < want && excl + mine >= want) {   // one thread of the block
+      int bin = b4 + 3, up = excl, here = c.w;
+      const int cc[3] = {c.z, c.y, c.x};
+#pragma unroll
+      for (int u = 0; u < 3; ++u)
+        if (up + here < want) {
+          up += here;
+          here = cc[u];
+          --bin;
+        }
+      found_bin = bin;
+      found_above = up;
+      found_count = here;
+    }
+    __syncthreads();
+  };
+  // a thread's smallest key - 1 (0 wraps to the largest), largest and number -> the cluster's smallest,
+  // largest and number; and whether any thread of it met a bad page
+  auto publish = [&](PsShared& to, uint32_t& kmin, uint32_t& kmax, int& valid) {
+    kmin = __reduce_min_sync(0xffffffffu, kmin);
+    kmax = __reduce_max_sync(0xffffffffu, kmax);
+    valid = __reduce_add_sync(0xffffffffu, valid);
+    const bool wbad = __any_sync(0xffffffffu, bad);
+    if (lane == 0) {
+      atomicMin(&to.kmin, kmin);
+      atomicMax(&to.kmax, kmax);
+      atomicAdd(&to.valid, valid);
+      if (wbad) to.bad = 1;
+    }
+    all_sync();
+    PsShared o[kPsMaxCluster];
+#pragma unroll
+    for (int r = 0; r < kPsMaxCluster; ++r)
+      if (r < C) {
+        const PsShared* q = cl.map_shared_rank(&to, r);
+        o[r].kmin = q->kmin; o[r].kmax = q->kmax; o[r].valid = q->valid; o[r].bad = q->bad;
+      }
+    kmin = o[0].kmin; kmax = o[0].kmax; valid = o[0].valid; bad = o[0].bad != 0;
+#pragma unroll
+    for (int r = 1; r < kPsMaxCluster; ++r)
+      if (r < C) {
+        kmin = min(kmin, o[r].kmin);
+        kmax = max(kmax, o[r].kmax);
+        valid += o[r].valid;
+        bad = bad || o[r].bad != 0;
+      }
+    ++kmin;
+  };
+  constexpr int kU = 8;   // 16-byte loads of a thread in flight
   uint32_t kmin = 0xffffffffu, kmax = 0u;
   int valid = 0;
   auto note = [&](uint32_t k) {
-    if (k != 0u) {
-      kmin = min(kmin, k);
-      kmax = max(kmax, k);
-      ++valid;
-    }
+    kmin = min(kmin, k - 1u);
+    kmax = max(kmax, k);
+    valid += k != 0u;
   };
-  {
-    constexpr int kU = 4;   // 16-byte loads of a thread in flight
-    for (int q0 = tid; q0 * 4 < ns; q0 += kPsThreads * kU) {
+
+  // ---- sieve
+  int* index = reinterpret_cast<int*>(keys + list_cap);                       // beside the list's keys
+  uint16_t* again = reinterpret_cast<uint16_t*>(keys + 2 * list_cap);         // [list_cap] groups to read again
+  int nb = 0;                                                                 // batches of the list
+  if (SIEVE && n >= 2 * kPsGroup * W) {
+    float* maxima = reinterpret_cast<float*>(keys);   // where the list will be
+    const float nothing = __int_as_float(0x7fffffff);
+    // values at i .. i + 3 of the stretch; a NaN where there is none (it passes no comparison)
+    auto values4 = [&](int i) -> float4 {
+      if (i >= ns) return make_float4(nothing, nothing, nothing, nothing);
+      float4 f = value4(i0 + i);
+      if (i + 1 >= ns) f.y = nothing;
+      if (i + 2 >= ns) f.z = nothing;
+      if (i + 3 >= ns) f.w = nothing;
+      return f;
+    };
+    float fmin = INFINITY, fmax = -INFINITY;
+    for (int c0 = warp * 1024; c0 < ns; c0 += NW * 1024) {   // 1024 neighbouring keys of a warp
+      float4 f[kU];
+      const int i = c0 + lane * 4, pos = i0 + i;
+      if (c0 + 1024 <= ns && (((i0 + c0 + 1023) >> P.page_shift) - tab0) < page_cap) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int pu = pos + u * 128;
+          f[u] = *reinterpret_cast<const float4*>(P.delta + (pu & (page - 1)) +
+                                                  ((size_t)pages[(pu >> P.page_shift) - tab0] << P.page_shift));
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) f[u] = values4(i + u * 128);
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        float m = fmaxf(fmaxf(f[u].x, f[u].y), fmaxf(f[u].z, f[u].w));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        if ((lane & 1) == 0) {
+          maxima[(i + u * 128) >> 3] = m;
+          valid += m == m;
+        }
+        fmin = fminf(fmin, m);
+        fmax = fmaxf(fmax, m);
+      }
+    }
+    if (fmin <= fmax) {
+      kmin = order_key(fmin) - 1u;
+      kmax = order_key(fmax);
+    }
+    publish(msh, kmin, kmax, valid);
+    // more groups than keys wanted, or no bound
+    if (!bad && valid >= W) {
+      const uint32_t range = kmax - kmin;
+      const int shift = range == 0u ? 0 : max(0, 32 - LB - __clz(range));
+      const int ng = (ns + kPsGroup - 1) / kPsGroup;
+      for (int i = tid; i < ng; i += NT) {
+        const float m = maxima[i];
+        if (m == m) atomicAdd(&mhist[(order_key(m) - kmin) >> shift], 1);
+      }
+      all_sync();
+      find_bin(mhist, 0, W, wbuf[0]);
+      // at least W keys are no smaller than this one
+      const uint32_t lk = kmin + ((uint32_t)found_bin << shift);
+      const float least = __uint_as_float((lk & 0x80000000u) ? lk ^ 0x80000000u : ~lk);
+      // the groups that reach it, in order: a warp counts and writes those of its stretch
+      const unsigned lt = (1u << lane) - 1u;
+      const int gpw = ((ng + NW - 1) / NW + 31) & ~31, g0 = min(warp * gpw, ng), g1 = min(g0 + gpw, ng);
+      int hits = 0;
+#pragma unroll 4
+      for (int i = g0; i < g1; i += 32)
+        hits += __popc(__ballot_sync(0xffffffffu, i + lane < g1 && maxima[i + lane] >= least));
+      const int2 wb = warps_before<NW>(hits, wbuf[1]);
+      const int n_again = wb.y;
+      const bool many = n_again > list_cap;   // many keys alike: the list would not hold them
+      if (!many) {
+        int at = wb.x;
+#pragma unroll 4
+        for (int i = g0; i < g1; i += 32) {
+          const bool hit = i + lane < g1 && maxima[i + lane] >= least;
+          const unsigned m = __ballot_sync(0xffffffffu, hit);
+          if (hit) again[at + __popc(m & lt)] = (uint16_t)(i + lane);
+          at += __popc(m);
+        }
+      }
+      __syncthreads();
+      // they are read again, 128 groups (four a lane) together: a place in the list for their keys, written
+      // there in the order of positions (the places of different batches come in any order)
+      nb = many ? 0 : (n_again + 127) >> 7;
+      for (int bt = warp; bt < nb; bt += NW) {
+        float4 f[kU];
+        int from[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int it = bt * 128 + u * 32 + lane;
+          from[u] = it < n_again ? again[it] * kPsGroup : ns;
+          f[2 * u] = values4(from[u]);
+          f[2 * u + 1] = values4(from[u] + 4);
+        }
+        unsigned own[4];
+        int mine = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float4 a = f[2 * u], c = f[2 * u + 1];
+          own[u] = (unsigned)(a.x >= least) | (unsigned)(a.y >= least) << 1 | (unsigned)(a.z >= least) << 2 |
+                   (unsigned)(a.w >= least) << 3 | (unsigned)(c.x >= least) << 4 | (unsigned)(c.y >= least) << 5 |
+                   (unsigned)(c.z >= least) << 6 | (unsigned)(c.w >= least) << 7;
+          mine += __popc(own[u]);
+        }
+        const int total = __reduce_add_sync(0xffffffffu, mine);
+        int first = 0;
+        if (lane == 0) {
+          first = atomicAdd(&listed_total, total);
+          batch[bt] = make_int2(first, total);
+        }
+        first = __shfl_sync(0xffffffffu, first, 0);
+        if (first + total > list_cap) continue;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int c = __popc(own[u]);
+          int incl = c;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+          }
+          int at = first + incl - c;
+          while (own[u] != 0u) {   // nearly always one
+            const int e = __ffs(own[u]) - 1;
+            const float4 q = e < 4 ? f[2 * u] : f[2 * u + 1];
+            const float v = (e & 3) == 0 ? q.x : (e & 3) == 1 ? q.y : (e & 3) == 2 ? q.z : q.w;
+            keys[at] = order_key(v);
+            index[at++] = i0 + from[u] + e;
+            own[u] &= own[u] - 1u;
+          }
+          first += __shfl_sync(0xffffffffu, incl, 31);
+        }
+      }
+      __syncthreads();
+      items = listed_total;
+      if (tid == 0 && (many || items > list_cap)) sh.members = 1;
+      if (items <= list_cap && tid < ((items + 3) & ~3) - items) keys[items + tid] = 0u;   // read four at a time
+      // bounds of the list's keys and their number
+      kmin = lk - 1u;
+      valid = tid == 0 ? items : 0;
+      publish(sh, kmin, kmax, valid);
+      sieved = true;
+      for (int r = 0; r < C; ++r) sieved = sieved && cl.map_shared_rank(&sh, r)->members == 0;
+    }
+    if (!sieved) {
+      all_sync();                          // all have seen it
+      if (tid == 0) {
+        sh.kmin = 0xffffffffu;
+        sh.kmax = 0u;
+        sh.valid = 0;
+        sh.members = 0;
+      }
+      __syncthreads();
+      items = ns;
+      kmin = 0xffffffffu;
+      kmax = 0u;
+      valid = 0;
+    } else {
+      res = items;
+    }
+  }
+
+  // ---- read the stretch: keys, smallest, largest, how many
+  if (!SIEVE || !sieved) {
+    for (int q0 = tid; q0 * 4 < ns; q0 += NT * kU) {
       uint4 k[kU];
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        const int i = (q0 + u * kPsThreads) * 4;
+        const int i = (q0 + u * NT) * 4;
         k[u] = i < ns ? load4(i0 + i) : make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        const int i = (q0 + u * kPsThreads) * 4;
-        if (i < cap) *reinterpret_cast<uint4*>(keys + i) = k[u];
+        const int i = (q0 + u * NT) * 4;
+        if (i < min(ns, cap)) *reinterpret_cast<uint4*>(keys + i) = k[u];
         note(k[u].x); note(k[u].y); note(k[u].z); note(k[u].w);
       }
     }
-  }
-  kmin = __reduce_min_sync(0xffffffffu, kmin);
-  kmax = __reduce_max_sync(0xffffffffu, kmax);
-  valid = __reduce_add_sync(0xffffffffu, valid);
-  const bool wbad = __any_sync(0xffffffffu, bad);
-  if (lane == 0) {
-    atomicMin(&sh.kmin, kmin);
-    atomicMax(&sh.kmax, kmax);
-    atomicAdd(&sh.valid, valid);
-    if (wbad) sh.bad = 1;
-  }
-  for (int i = tid; i < 2 * kPsBins; i += kPsThreads) (&hist[0][0])[i] = 0;
-  cl.sync();
-  valid = 0;
-  bad = false;
-  for (int r = 0; r < C; ++r) {
-    const PsShared* o = cl.map_shared_rank(&sh, r);
-    kmin = r == 0 ? o->kmin : min(kmin, o->kmin);
-    kmax = r == 0 ? o->kmax : max(kmax, o->kmax);
-    valid += o->valid;
-    bad = bad || o->bad != 0;
+    publish(sh, kmin, kmax, valid);
   }
   if (tid == 0 && rank == 0) {
     if (M != kCandidates) counters[row] = 0;
@@ -168,101 +456,144 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
     uint32_t lo = kmin, span = 0xffffffffu;   // the edge lies in [lo, lo + span]
     int above = 0;                            // keys above that interval
     const uint32_t range = kmax - kmin;
-    int shift = range == 0u ? 0 : max(0, 21 - __clz(range));
-    if (range == 0u) T = kmin;
-    for (int round = 0; range != 0u; ++round) {
-      int* hs = hist[round & 1];
-      if (round >= 2) {
-        for (int i = tid; i < kPsBins; i += kPsThreads) hs[i] = 0;   // all have read it: they synced since
-        __syncthreads();
-      }
-      for (int i = tid; i < ns; i += kPsThreads) {
-        const uint32_t k = key_at(i);
-        if (k >= lo && k - lo <= span) atomicAdd(&hs[(k - lo) >> shift], 1);
-      }
-      cl.sync();
-      // thread t sums counters 4t' .. 4t'+3 over the cluster, from the top: t' = 511 - t
-      const int b4 = (kPsThreads - 1 - tid) * 4;
-      int4 c = make_int4(0, 0, 0, 0);
-      for (int r = 0; r < C; ++r) {
-        const int4 o = *reinterpret_cast<const int4*>(cl.map_shared_rank(hs + b4, r));
-        c.x += o.x; c.y += o.y; c.z += o.z; c.w += o.w;
-      }
-      const int mine = c.x + c.y + c.z + c.w;
-      int incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      if (lane == 31) wsum[warp][0] = incl;
-      __syncthreads();
-      int before = above;
-      for (int w = 0; w < warp; ++w) before += wsum[w][0];
-      const int excl = before + incl - mine;
-      if (excl < W && excl + mine >= W) {   // one thread of the block
-        int bin = b4 + 3, up = excl;
-        const int cc[4] = {c.w, c.z, c.y, c.x};
-#pragma unroll
-        for (int u = 0; u < 3; ++u)
-          if (bin == b4 + 3 - u && up + cc[u] < W) {
-            up += cc[u];
-            --bin;
-          }
-        found_bin = bin;
-        found_above = up;
-      }
-      __syncthreads();
+    int shift = range == 0u ? 0 : max(0, 32 - LB - __clz(range));
+    T = kmin;
+    while (range != 0u) {
+      for_keys([&](uint32_t k) {
+        if (k >= lo && k - lo <= span) atomicAdd(&hist[(k - lo) >> shift], 1);
+      });
+      all_sync();
+      find_bin(hist, above, W, wbuf[0]);
       above = found_above;
       lo += (uint32_t)found_bin << shift;
-      if (shift == 0) {
-        T = lo;
+      T = lo;
+      if (shift == 0) break;
+      span = (1u << shift) - 1u;
+      if (found_count <= NT) {
+        // rank the interval's keys against each other
+        for_keys([&](uint32_t k) {
+          if (k >= lo && k - lo <= span) list[atomicAdd(&sh.members, 1)] = k;
+        });
+        all_sync();
+        int m = 0;
+        for (int r = 0; r < C; ++r) {
+          const int mr = cl.map_shared_rank(&sh, r)->members;
+          if (tid < mr) every[m + tid] = *cl.map_shared_rank(list + tid, r);
+          m += mr;
+        }
+        __syncthreads();
+        if (tid < m) {
+          const uint32_t k = every[tid];
+          int gt = above, ge = above;
+          for (int i = 0; i < m; ++i) {
+            const uint32_t o = every[i];
+            gt += o > k;
+            ge += o >= k;
+          }
+          if (gt < W && ge >= W) {   // the edge's holders, all alike
+            found_key = k;
+            found_above = gt;
+          }
+        }
+        __syncthreads();
+        above = found_above;
+        T = found_key;
         break;
       }
-      span = (1u << shift) - 1u;
-      shift = max(0, shift - 11);
+      shift = max(0, shift - LB);
+      all_sync();   // every CTA has read the counters
+      *reinterpret_cast<int4*>(hist + 4 * tid) = make_int4(0, 0, 0, 0);
+      __syncthreads();
     }
     need = W - above;
   }
   if (bad || idle) T = 0xffffffffu;
 
-  // ---- counts of this CTA's warps: contiguous stretches of whole 32s
-  const int per = ((ns + kPsWarps - 1) / kPsWarps + 31) & ~31;
-  const int j0 = min(warp * per, ns), j1 = min(j0 + per, ns);
+  // ---- counts of this CTA's warps: contiguous stretches, four neighbouring keys a lane
+  const int per = ((items + NW - 1) / NW + 127) & ~127;
+  const int j0 = min(warp * per, items), j1 = min(j0 + per, items);
   int cnt[4] = {0, 0, 0, 0};   // as PsShared::count
-  if (!bad)
-    for (int j = j0 + lane; j < j1; j += 32) {
-      const uint32_t k = key_at(j);
-      const int at = M == kRest && i0 + j < n1p ? 0 : 2;
-      cnt[at] += k > T;
-      cnt[at + 1] += k == T && k != 0u;
+  if (SIEVE && sieved) {
+    // batches instead of stretches
+    for (int bt = warp; bt < nb; bt += NW) {
+      const int2 bb = batch[bt];
+      int gt = 0, eq = 0;
+      for (int j = lane; j < bb.y; j += 32) {
+        const uint32_t k = keys[bb.x + j];
+        gt += k > T;
+        eq += k == T;
+      }
+      gt = __reduce_add_sync(0xffffffffu, gt);
+      eq = __reduce_add_sync(0xffffffffu, eq);
+      if (lane == 0) batch_in[bt] = make_int2(gt, eq);
     }
+    __syncthreads();
+    int2 own = make_int2(0, 0);
+    if (tid < nb) own = batch_in[tid];
+    int2 incl = own;
 #pragma unroll
-  for (int u = 0; u < 4; ++u) cnt[u] = __reduce_add_sync(0xffffffffu, cnt[u]);
-  if (lane == 0) {
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
+      if (lane >= o) {
+        incl.x += x;
+        incl.y += y;
+      }
+    }
+    const int2 wx = warps_before<NW>(__shfl_sync(0xffffffffu, incl.x, 31), wbuf[1]);
+    const int2 wy = warps_before<NW>(__shfl_sync(0xffffffffu, incl.y, 31), wbuf[2]);
+    if (tid < nb) batch_in[tid] = make_int2(wx.x + incl.x - own.x, wy.x + incl.y - own.y);
+    if (tid == 0) cnt[2] = wx.y, cnt[3] = wy.y;   // the CTA's, for the sums over the cluster
+  } else if (!bad) {
+#pragma unroll 4
+    for (int j = j0 + lane * 4; j < j1; j += 128) {
+      const uint4 k4 = keys4(j);
+      const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+      const bool c = M == kRest && i0 + j < n1p;   // n1p and j are multiples of 4
 #pragma unroll
-    for (int u = 0; u < 4; ++u) wsum[warp][u] = cnt[u];
-  }
-  __syncthreads();
-  if (tid < 4) {
-    int s = 0;
-    for (int w = 0; w < kPsWarps; ++w) s += wsum[w][tid];
-    reinterpret_cast<int*>(&sh.count)[tid] = s;
-  }
-  cl.sync();
-  int all[4] = {0, 0, 0, 0}, mine[4] = {0, 0, 0, 0};   // over the cluster; before this warp
-  for (int r = 0; r < C; ++r) {
-    const int4 o = cl.map_shared_rank(&sh, r)->count;
-    const int oc[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      all[u] += oc[u];
-      if (r < rank) mine[u] += oc[u];
+      for (int u = 0; u < 4; ++u) {
+        const int gt = k[u] > T, eq = k[u] == T && T != 0u;
+        if (M == kRest) {
+          cnt[0] += c ? gt : 0;
+          cnt[1] += c ? eq : 0;
+        }
+        cnt[2] += c ? 0 : gt;
+        cnt[3] += c ? 0 : eq;
+      }
     }
   }
-  for (int w = 0; w < warp; ++w)
+  int2 cta_in = make_int2(0, 0);                // above and at the edge in the CTAs before this one
+  int mine[4], tot[4], all[4] = {0, 0, 0, 0};   // before this warp; over the CTA; over the cluster
 #pragma unroll
-    for (int u = 0; u < 4; ++u) mine[u] += wsum[w][u];
+  for (int u = M == kRest ? 0 : 2; u < 4; ++u) {
+    const int2 v = warps_before<NW>(__reduce_add_sync(0xffffffffu, cnt[u]), wbuf[1 + u]);
+    mine[u] = v.x;
+    tot[u] = v.y;
+  }
+  if (M != kRest) mine[0] = mine[1] = tot[0] = tot[1] = 0;
+  if (C > 1) {
+    if (tid == 0) sh.count = make_int4(tot[0], tot[1], tot[2], tot[3]);
+    cl.sync();
+    int4 o[kPsMaxCluster];
+#pragma unroll
+    for (int r = 0; r < kPsMaxCluster; ++r)
+      o[r] = r < C ? cl.map_shared_rank(&sh, r)->count : make_int4(0, 0, 0, 0);
+#pragma unroll
+    for (int r = 0; r < kPsMaxCluster; ++r) {
+      const int oc[4] = {o[r].x, o[r].y, o[r].z, o[r].w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        all[u] += oc[u];
+        if (r < rank) mine[u] += oc[u];
+      }
+      if (r < rank) {
+        cta_in.x += o[r].z;
+        cta_in.y += o[r].w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) all[u] = tot[u];
+  }
   const int ties_c = min(need, all[1]);   // ties taken among the candidates
   int32_t* rec = M == kCandidates ? crow + h : rows + (size_t)row * 4;
   if (rank == 0 && tid == 0) {
@@ -279,51 +610,95 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
   }
 
   // ---- the list
-  if (!bad) {
+  if (SIEVE && sieved) {
+    const int gt0 = cta_in.x, eq0 = cta_in.y;
+    int32_t* lp = sel + (size_t)row * P.sel_len;
+    int2* le = ent + (size_t)row * P.sel_len;
+    const unsigned lt = (1u << lane) - 1u;
+    for (int bt = warp; bt < nb; bt += NW) {
+      const int2 bb = batch[bt], in = batch_in[bt];
+      int eq = eq0 + in.y, out = gt0 + in.x + min(need, eq);
+      for (int j = lane; j - lane < bb.y; j += 32) {
+        const uint32_t k = j < bb.y ? keys[bb.x + j] : 0u;
+        const unsigned em = __ballot_sync(0xffffffffu, k == T);   // T is a key of the row, not 0
+        const bool take = k > T || (k == T && eq + __popc(em & lt) < need);
+        const unsigned tm = __ballot_sync(0xffffffffu, take);
+        if (take) {
+          const int at = out + __popc(tm & lt), pos = index[bb.x + j];
+          lp[at] = pos;
+          le[at] = make_int2(slot_of(pos), (int)((k & 0x80000000u) ? k ^ 0x80000000u : ~k));
+        }
+        eq += __popc(em);
+        out += __popc(tm);
+      }
+    }
+  } else if (!bad) {
     int eq = mine[1] + mine[3];                            // ties before this warp's keys
     int out = mine[2] + max(0, min(need, eq) - ties_c);    // listed keys before them
     int32_t* lp = M == kCandidates ? cand + (size_t)h * P.cand_len : sel + (size_t)row * P.sel_len;
     int2* le = M == kCandidates ? cent + (size_t)h * P.cand_len : ent + (size_t)row * P.sel_len;
     const unsigned lt = (1u << lane) - 1u;
-    for (int j = j0; j < j1; j += 32) {
-      const int i = i0 + j + lane;
-      const uint32_t k = j + lane < j1 ? key_at(j + lane) : 0u;
-      const bool is_eq = k == T && k != 0u;
-      const unsigned em = __ballot_sync(0xffffffffu, is_eq);
-      const int tie = eq + __popc(em & lt);
-      const bool take = k > T || (is_eq && tie < need);
-      if (M == kRest && is_eq && i < n1p && tie == need - 1 && ties_c < all[1]) rec[2] = i + 1;
-      const bool list = take && !(M == kRest && i < n1p);
-      const unsigned lm = __ballot_sync(0xffffffffu, list);
-      if (list) {
-        const int at = out + __popc(lm & lt), pos = base + i - n1p;
-        const int slot = (__ldg(tab + (pos >> P.page_shift)) << P.page_shift) + (pos & (page - 1));
-        lp[at] = pos;
-        le[at] = make_int2(slot, (int)((k & 0x80000000u) ? k ^ 0x80000000u : ~k));
+    for (int j = j0; j < j1; j += 128) {
+      const int jl = j + lane * 4, i = i0 + jl;
+      const uint4 k4 = jl < j1 ? keys4(jl) : make_uint4(0u, 0u, 0u, 0u);
+      const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+      const bool c = M == kRest && i < n1p;
+      bool take[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) take[u] = k[u] > T && !c;
+      const bool has = T != 0u && (k[0] == T || k[1] == T || k[2] == T || k[3] == T);
+      if (__any_sync(0xffffffffu, has)) {   // ties, in the order of positions
+        int before = eq, sum = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const unsigned em = __ballot_sync(0xffffffffu, k[u] == T);
+          before += __popc(em & lt);
+          sum += __popc(em);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (k[u] == T) {
+            if (!c) take[u] = before < need;
+            else if (before == need - 1 && ties_c < all[1]) rec[2] = i + u + 1;
+            ++before;
+          }
+        eq += sum;
       }
-      eq += __popc(em);
-      out += __popc(lm);
+      unsigned tm[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) tm[u] = __ballot_sync(0xffffffffu, take[u]);
+      if ((tm[0] | tm[1] | tm[2] | tm[3]) == 0u) continue;
+      int at = out + __popc(tm[0] & lt) + __popc(tm[1] & lt) + __popc(tm[2] & lt) + __popc(tm[3] & lt);
+      out += __popc(tm[0]) + __popc(tm[1]) + __popc(tm[2]) + __popc(tm[3]);
+      if (take[0] || take[1] || take[2] || take[3]) {
+        const int pos = base + i - n1p;   // all four on one page
+        const int slot = slot_of(pos);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (take[u]) {
+            lp[at] = pos + u;
+            le[at] = make_int2(slot + u, (int)((k[u] & 0x80000000u) ? k[u] ^ 0x80000000u : ~k[u]));
+            ++at;
+          }
+      }
     }
   }
-  cl.sync();   // no CTA leaves while another may still read its shared memory
+  if (C > 1) cl.sync();   // no CTA leaves while another may still read its shared memory
 }
 
-// Launches the selection of `n_rows` rows of at most n values.  Clusters: stretches of at most 16384
-// values (64 KB, three CTAs an SM), and for few rows as many CTAs as give every SM one, down to stretches
-// of 2048.
-template <SelMode M>
-cudaError_t launch_select(const PagedPlan& P, int n_rows, int n, void* ws, cudaStream_t s) {
-  int C = 1;
-  const int sms = sm_count();
-  while (C < kPsMaxCluster && ((n + C - 1) / C > 16384 || (n_rows * C < sms && (n + C - 1) / C > 2048))) C *= 2;
-  int cap = (((n + C - 1) / C + 3) & ~3) + 4;
-  if (cap > 49152) cap = 49152;
-  const size_t smem = (size_t)cap * 4;
-  const cudaError_t e = ensure_smem_limit(paged_select_kernel<M>, (int)smem);
+// cap: words of shared memory for keys.
+template <SelMode M, int NT, bool SIEVE>
+cudaError_t launch_select_t(const PagedPlan& P, int n_rows, int n, int C, int cap, int list_cap, void* ws,
+                            cudaStream_t s) {
+  const int seg = ((n + C - 1) / C + 3) & ~3;
+  int page_cap = (seg >> P.page_shift) + 2;
+  if (page_cap > 4096) page_cap = 4096;
+  const size_t smem = (size_t)(cap + page_cap) * 4;
+  const cudaError_t e = ensure_smem_limit(paged_select_kernel<M, NT, SIEVE>, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(C, n_rows);
-  cfg.blockDim = dim3(kPsThreads);
+  cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -333,11 +708,39 @@ cudaError_t launch_select(const PagedPlan& P, int n_rows, int n, void* ws, cudaS
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_select_kernel<M>, P, ws_ptr<int32_t>(ws, P.off_rows),
+  return cudaLaunchKernelEx(&cfg, paged_select_kernel<M, NT, SIEVE>, P, ws_ptr<int32_t>(ws, P.off_rows),
                             ws_ptr<int32_t>(ws, P.off_sel), ws_ptr<int2>(ws, P.off_ent),
                             ws_ptr<int32_t>(ws, P.off_crow), ws_ptr<int32_t>(ws, P.off_cand),
                             ws_ptr<int2>(ws, P.off_cent), ws_ptr<int32_t>(ws, P.off_count),
-                            ws_ptr<int32_t>(ws, P.off_status), cap);
+                            ws_ptr<int32_t>(ws, P.off_status), cap, page_cap, list_cap);
+}
+
+// Launches the selection of `n_rows` rows of at most n values.
+template <SelMode M>
+cudaError_t launch_select(const PagedPlan& P, int n_rows, int n, void* ws, cudaStream_t s) {
+  const int sms = sm_count();
+  if constexpr (M == kRows) {
+    // rows that would take the kernel below several waves of stretches
+    if (n >= 16384 && n >= 2 * kPsGroup * (int64_t)P.w && (int64_t)n_rows * n > (int64_t)sms * 16384) {
+      int C = 1;
+      while (C < kPsMaxCluster && ((n + C - 1) / C > 65536 || n_rows * C < sms)) C *= 2;
+      const int seg = ((n + C - 1) / C + 3) & ~3;
+      // the list: twice the window, and room for the maxima (two words an entry) first
+      int list_cap = 2 * P.w + 2048;
+      if (list_cap < seg / (2 * kPsGroup) + 64) list_cap = seg / (2 * kPsGroup) + 64;
+      list_cap = (list_cap + 7) & ~7;
+      const int cap = 2 * list_cap + list_cap / 2;
+      if (seg <= 65536 && list_cap <= 128 * kPsMaxBatches && cap <= 36864)
+        return launch_select_t<M, 512, true>(P, n_rows, n, C, cap, list_cap, ws, s);
+    }
+  }
+  // clusters: stretches of at most 16384 values, and for few rows as many CTAs as give every SM one, down to
+  // stretches of 2048; short rows in large numbers go to small CTAs, more of which share an SM
+  int C = 1;
+  while (C < kPsMaxCluster && ((n + C - 1) / C > 16384 || (n_rows * C < sms && (n + C - 1) / C > 2048))) C *= 2;
+  const int seg = ((n + C - 1) / C + 3) & ~3, cap = seg + 4 < 40960 ? seg + 4 : 40960;
+  if (seg <= 4096 && n_rows * C >= 4 * sms) return launch_select_t<M, 128, false>(P, n_rows, n, C, cap, 0, ws, s);
+  return launch_select_t<M, 512, false>(P, n_rows, n, C, cap, 0, ws, s);
 }
 
 }  // namespace
