@@ -6,9 +6,9 @@
 //
 // paged_list_kernel takes a row's own list.  The rows it needs lie anywhere in the cache, so what bounds
 // it is how many 256-byte reads are in flight: a group of d / 8 lanes handles one key at a time (K and V
-// row, 16 bytes a lane), a warp has the rows of 8 keys for each of its groups on the way at once, all in
-// registers, and nothing waits for another warp before the end.  Each group keeps its own running maximum
-// and sum; they meet once per CTA.
+// row, 16 bytes a lane), and the rows of the next keys are always on their way into a ring of shared
+// memory.  Every lane reads back just what it copied itself, so nothing waits for another warp before the
+// end.  Each group keeps its own running maximum and sum; they meet once per CTA.
 // paged_cand_kernel (shared prefix) multiplies all sequences' queries of a head with the head's
 // candidates: 16 x 64 score tiles on the tensor cores, a sequence's selection being a comparison of the
 // candidate's delta with the edge of its row.
@@ -43,22 +43,61 @@ DMA_DEVINL void join_row(const float* part, int n, T* O, float* LSE) {
   }
 }
 
-template <typename T, int D, int U>
-__global__ void __launch_bounds__(kPlThreads)
+constexpr int kPlStages = 3;
+
+template <typename T> constexpr int list_keys() { return sizeof(T) == 2 ? 4 : 2; }   // keys of a group and stage
+// bytes of the ring: stages x keys x (K, V) x eight channels of every thread
+template <typename T> constexpr int list_smem() { return kPlStages * list_keys<T>() * 2 * 8 * sizeof(T) * kPlThreads; }
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kPlThreads, 4)
 paged_list_kernel(const T* __restrict__ Q, const T* __restrict__ K, const T* __restrict__ V,
                   const int4* __restrict__ rows, const int2* __restrict__ ent, float* __restrict__ part,
                   int32_t* __restrict__ counters, T* __restrict__ O, float* __restrict__ LSE, int H, int Hkv,
                   int page_shift, int sel_len, int n_split, int n_psplit, float scale) {
   constexpr int L = D / 8, RPW = 32 / L, NG = kPlWarps * RPW;   // lanes of a row; groups of a warp, of the CTA
-  __shared__ float so[NG][D];
+  constexpr int U = list_keys<T>(), NP = sizeof(T) / 2;         // 16-byte pieces of a lane's eight channels
+  static_assert(kPagedSplit / NG <= 2 * L, "two entries a lane hold a group's keys");
+  static_assert(list_smem<T>() >= NG * D * 4, "the ring's place takes the groups' results at the end");
+  extern __shared__ __align__(128) unsigned char ring[];
+  float* so = reinterpret_cast<float*>(ring);   // [NG][D], when the ring is done with
   __shared__ float sm[NG], sl[NG];
   __shared__ int last;
   const int row = blockIdx.y, h = row % H, g = h / (H / Hkv);
   const int tid = threadIdx.x, lane = tid & 31, grp = tid / L, e = (lane % L) * 8;
   const int count = min(rows[row].x, sel_len);
-  const int k0 = blockIdx.x * kPagedSplit, k1 = min(count, k0 + kPagedSplit);
-  if (k0 >= count && blockIdx.x > 0) return;   // the first CTA of a row works even if there is nothing
-  const int2* list = ent + (size_t)row * sel_len;
+  const int k0 = blockIdx.x * kPagedSplit, nk = min(count - k0, kPagedSplit);
+  if (nk <= 0 && blockIdx.x > 0) return;   // the first CTA of a row works even if there is nothing
+  // the group's keys: k0 + j NG + grp; lane i of it holds the entries of j = i and i + L
+  const int2* list = ent + (size_t)row * sel_len + k0;
+  int2 en[2] = {make_int2(0, 0), make_int2(0, 0)};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int k = (lane % L + i * L) * NG + grp;
+    if (k < nk) en[i] = list[k];
+  }
+  const int mask = (1 << page_shift) - 1;
+  const uint32_t mine = smem_u32(ring) + tid * 16;
+  auto issue = [&](int st) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = st * U + u, n = j * NG + grp < nk ? 16 : 0;
+      const int slot = __shfl_sync(0xffffffffu, j < L ? en[0].x : en[1].x, j % L, L);
+      const size_t at = (((((size_t)(slot >> page_shift) * Hkv + g) << page_shift) + (slot & mask)) * D) + e;
+      const uint32_t to = mine + (((st % kPlStages) * U + u) * 2 * NP) * kPlThreads * 16;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        cp_async_16(to + i * kPlThreads * 16, K + at + i * 4, n);
+        cp_async_16(to + (NP + i) * kPlThreads * 16, V + at + i * 4, n);
+      }
+    }
+  };
+  const int ns = nk > 0 ? ((nk + NG - 1) / NG + U - 1) / U : 0;
+#pragma unroll
+  for (int st = 0; st < kPlStages - 1; ++st) {
+    if (st < ns) issue(st);
+    cp_async_commit();
+  }
   float q[8];
   widen8(load_raw8(Q + (size_t)row * D + e), q);
 #pragma unroll
@@ -66,38 +105,27 @@ paged_list_kernel(const T* __restrict__ Q, const T* __restrict__ K, const T* __r
   float m = -INFINITY, l = 0.f, acc[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-  const int mask = (1 << page_shift) - 1;
-  // group grp takes U keys at a time: k0 + (NG r + grp) U ..
-  for (int kb = k0 + (tid / 32) * RPW * U; kb < k1; kb += NG * U) {
-    const int mykey = kb + (lane / L) * U + (lane % L);   // lane i of the group fetches entry i
-    int2 en = make_int2(0, 0);
-    if (lane % L < U && mykey < k1) en = list[mykey];
-    Raw8<T> kr[U], vr[U];
-    float dl[U];
-    bool on[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int slot = __shfl_sync(0xffffffffu, en.x, u, L);
-      dl[u] = __int_as_float(__shfl_sync(0xffffffffu, en.y, u, L));
-      on[u] = kb + (lane / L) * U + u < k1;
-      const size_t at = (((((size_t)(slot >> page_shift) * Hkv + g) << page_shift) + (slot & mask)) * D) + e;
-      if (on[u]) {
-        kr[u] = load_raw8(K + at);
-        vr[u] = load_raw8(V + at);
-      } else {
-        kr[u] = Raw8<T>{};
-        vr[u] = Raw8<T>{};
-      }
-    }
+  for (int st = 0; st < ns; ++st) {
+    if (st + kPlStages - 1 < ns) issue(st + kPlStages - 1);
+    cp_async_commit();
+    cp_async_wait<kPlStages - 1>();
+    const unsigned char* from = ring + tid * 16 + ((st % kPlStages) * U * 2 * NP) * kPlThreads * 16;
     float x[U], mx = m;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      Raw8<T> raw;
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+        reinterpret_cast<uint4*>(&raw)[i] =
+            *reinterpret_cast<const uint4*>(from + (u * 2 * NP + i) * kPlThreads * 16);
       float k[8], s = 0.f;
-      widen8(kr[u], k);
+      widen8(raw, k);
 #pragma unroll
       for (int i = 0; i < 8; ++i) s = fmaf(k[i], q[i], s);
       s = row_sum<L>(s);
-      x[u] = on[u] ? s + dl[u] : -INFINITY;
+      const int j = st * U + u;
+      const float dl = __int_as_float(__shfl_sync(0xffffffffu, j < L ? en[0].y : en[1].y, j % L, L));
+      x[u] = j * NG + grp < nk ? s + dl : -INFINITY;
       mx = fmaxf(mx, x[u]);
     }
     const float ref = mx == -INFINITY ? 0.f : mx;
@@ -108,16 +136,22 @@ paged_list_kernel(const T* __restrict__ Q, const T* __restrict__ K, const T* __r
     for (int i = 0; i < 8; ++i) acc[i] *= keep;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      Raw8<T> raw;
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+        reinterpret_cast<uint4*>(&raw)[i] =
+            *reinterpret_cast<const uint4*>(from + (u * 2 * NP + NP + i) * kPlThreads * 16);
       const float p = exp_diff(x[u], ref);
       float v[8];
-      widen8(vr[u], v);
+      widen8(raw, v);
       l += p;
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[i] = fmaf(p, v[i], acc[i]);
     }
   }
+  __syncthreads();   // every lane is done with the ring
 #pragma unroll
-  for (int i = 0; i < 8; ++i) so[grp][e + i] = acc[i];
+  for (int i = 0; i < 8; ++i) so[grp * D + e + i] = acc[i];
   if (lane % L == 0) {
     sm[grp] = m;
     sl[grp] = l;
@@ -140,7 +174,7 @@ paged_list_kernel(const T* __restrict__ Q, const T* __restrict__ K, const T* __r
     for (int c = tid; c < D; c += kPlThreads) {
       float o = 0.f;
 #pragma unroll
-      for (int i = 0; i < NG; ++i) o = fmaf(so[i][c], w[i], o);
+      for (int i = 0; i < NG; ++i) o = fmaf(so[i * D + c], w[i], o);
       if (n_act + n_psplit == 1) {
         store_from_f32(O + (size_t)row * D + c, lsum > 0.f ? o / lsum : (lsum == 0.f ? 0.f : lsum));
         if (c == 0) LSE[row] = lsum > 0.f ? ref + logf(lsum) : (lsum == 0.f ? -INFINITY : lsum);
@@ -430,9 +464,11 @@ cudaError_t launch_cand_rows(const PagedPlan& P, const void* Q, void* ws, cudaSt
   return launch_cand<D, 4>(P, Q, ws, s);
 }
 
-template <typename T, int D, int U>
+template <typename T, int D>
 cudaError_t launch_list(const PagedPlan& P, const void* Q, void* ws, void* O, float* LSE, cudaStream_t s) {
-  paged_list_kernel<T, D, U><<<dim3(P.n_split, P.B * P.H), kPlThreads, 0, s>>>(
+  const cudaError_t e = ensure_smem_limit(paged_list_kernel<T, D>, list_smem<T>());
+  if (e != cudaSuccess) return e;
+  paged_list_kernel<T, D><<<dim3(P.n_split, P.B * P.H), kPlThreads, list_smem<T>(), s>>>(
       (const T*)Q, (const T*)P.K, (const T*)P.V, ws_ptr<int4>(ws, P.off_rows), ws_ptr<int2>(ws, P.off_ent),
       ws_ptr<float>(ws, P.off_part), ws_ptr<int32_t>(ws, P.off_count), (T*)O, LSE, P.H, P.Hkv, P.page_shift, P.sel_len,
       P.n_split, P.n_psplit, P.scale);
@@ -447,9 +483,9 @@ cudaError_t launch_paged_attn(const PagedPlan& P, const void* Q, void* ws, void*
     if (e != cudaSuccess) return e;
   }
   if (P.bf16)
-    return P.d == 128 ? launch_list<uint16_t, 128, 8>(P, Q, ws, O, LSE, s)
-                      : launch_list<uint16_t, 64, 8>(P, Q, ws, O, LSE, s);
-  return P.d == 128 ? launch_list<float, 128, 4>(P, Q, ws, O, LSE, s) : launch_list<float, 64, 4>(P, Q, ws, O, LSE, s);
+    return P.d == 128 ? launch_list<uint16_t, 128>(P, Q, ws, O, LSE, s)
+                      : launch_list<uint16_t, 64>(P, Q, ws, O, LSE, s);
+  return P.d == 128 ? launch_list<float, 128>(P, Q, ws, O, LSE, s) : launch_list<float, 64>(P, Q, ws, O, LSE, s);
 }
 
 }  // namespace dma
