@@ -384,7 +384,7 @@ typedef struct {
 /*
  * Forward.  q, k, v: strided as st says (H, Hkv, Hkv heads of d channels, dtype).  Out: Q [B, H, N, d],
  * K, V [B, Hkv, N, d] dtype, dense.  v and V may be NULL together.  p: B, H, Hkv, N, d and dtype are
- * used, Nq must equal N; N <= 2^24 (no other limit of the attention applies).  Outputs must not overlap inputs.
+ * used, Nq must equal N; N <= 2^24, B N < 2^31 (no other limit of the attention applies).  Outputs must not overlap inputs.
  */
 dma_status_t dma_prep(const dma_params_t* p, const dma_prep_t* r, const dma_prep_strides_t* st, const void* q,
                       const void* k, const void* v, void* Q, void* K, void* V, void* stream);

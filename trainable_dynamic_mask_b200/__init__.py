@@ -178,38 +178,54 @@ def cp_compact(p, prefix_len, n_prev, cands, delta, K, V, delta_c, Kc, Vc, pos_c
 
 # ---------------------------------------------------------------- projections to inputs
 
-def _here(*tensors):
-    """Every tensor given (None and raw addresses aside) lies on the current CUDA device."""
+def _storage(p):
+    """torch type of p's storage."""
     import torch
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and not isinstance(t, int) and t.get_device() != dev:
-            raise ValueError(f"tensors passed to libdma must be on the current device (cuda:{dev}); got {t.device}")
+    return torch.bfloat16 if p.dtype == DMA_BF16 else torch.float32
 
 
-def _shaped(name, t, shape, p=None):
-    """t (a tensor, or None) has the given shape and, with p, p's storage type; without, float32."""
-    if t is None or isinstance(t, int):
-        return
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have the shape {shape}, not {tuple(t.shape)}")
-    want = "torch.bfloat16" if p is not None and p.dtype == DMA_BF16 else "torch.float32"
-    if str(t.dtype) != want:
-        raise ValueError(f"{name} must be {want}, not {t.dtype}")
+def _stream_on(stream, dev):
+    """_stream, for the current device dev.  The address alone: a Stream object takes longer to make than
+    all of a small call's checks."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
 
 
-def _rows_ptr(name, t, shape, out, p):
-    """Address of a strided tensor of rows [.., heads, d]; its strides (all but the last) go into out."""
+def _dense(name, t, shape, dtype, dev):
+    """Address of a dense tensor of that shape and type on the current device dev (None: NULL)."""
     if t is None:
         return None
-    _shaped(name, t, shape, p)
-    st = t.stride()
-    if st[-1] != 1:
-        raise ValueError(f"{name}: the channels of a row must be contiguous")
-    n = len(shape) - 1
-    for i in range(n):
-        out[3 - n + i] = st[i] if shape[i] > 1 else 0
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _refuse(name, t, shape, dtype, dev)
+        raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+def _rows(name, t, shape, dtype, dev, out):
+    """Address of rows [.., heads, d] at any strides; the strides of all but the channels go into out."""
+    if t is None:
+        return None
+    st = t.stride()
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or st[-1] != 1:
+        _refuse(name, t, shape, dtype, dev)
+        raise ValueError(f"{name}: the channels of a row must be contiguous")
+    # a dimension of one element has no stride to speak of
+    out[2] = st[-2] if shape[-2] > 1 else 0
+    out[1] = st[-3] if shape[-3] > 1 else 0
+    if len(shape) == 4:
+        out[0] = st[0] if shape[0] > 1 else 0
+    return t.data_ptr()
+
+
+def _refuse(name, t, shape, dtype, dev):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current device (cuda:{dev}), not {t.device}")
 
 
 def make_prep(inv_freq, q_weight=None, k_weight=None, eps=1e-6, positions=None, first=0, interleaved=False) -> DmaPrep:
@@ -220,44 +236,47 @@ def make_prep(inv_freq, q_weight=None, k_weight=None, eps=1e-6, positions=None, 
     norm.  positions: device int32 [B, N]; None: first, first + 1, ...  interleaved: the
     pairs are neighbouring channels instead of the two halves.  The result keeps the
     tensors alive."""
+    import torch
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    r = DmaPrep(inv_freq=_ptr(inv_freq), positions=_ptr(positions), q_weight=_ptr(q_weight), k_weight=_ptr(k_weight),
-                eps=float(eps), rot=rot, interleaved=1 if interleaved else 0, first=int(first))
-    _shaped("inv_freq", inv_freq, (rot // 2,))
-    if positions is not None and str(positions.dtype) != "torch.int32":
-        raise ValueError(f"positions must be torch.int32, not {positions.dtype}")
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    r = DmaPrep(inv_freq=_dense("inv_freq", inv_freq, (rot // 2,), torch.float32, dev), eps=float(eps), rot=rot,
+                interleaved=1 if interleaved else 0, first=int(first))
+    r.q_weight, r.k_weight, r.positions = _ptr(q_weight), _ptr(k_weight), _ptr(positions)
     r.tensors = (inv_freq, q_weight, k_weight, positions)
+    r.fits = None
     return r
 
 
-def _check_prep_tensors(p, r):
-    _, qw, kw, pos = r.tensors
-    _shaped("q_weight", qw, (p.d,), p)
-    _shaped("k_weight", kw, (p.d,), p)
-    if pos is not None and tuple(pos.shape) != (p.B, p.N):
-        raise ValueError(f"positions must have the shape {(p.B, p.N)}, not {tuple(pos.shape)}")
+def _check_prep_tensors(p, r, dev):
+    """The weights and positions of r fit p (looked at again when p's sizes change)."""
+    import torch
+    key = (p.B, p.N, p.d, p.dtype, dev)
+    if r.fits != key:
+        _, qw, kw, pos = r.tensors
+        _dense("q_weight", qw, (p.d,), _storage(p), dev)
+        _dense("k_weight", kw, (p.d,), _storage(p), dev)
+        _dense("positions", pos, (p.B, p.N), torch.int32, dev)
+        r.fits = key
 
 
 def prep(p, r, q, k, v, Q, K, V, stream=None):
     """Projections q [B, N, H, d], k, v [B, N, Hkv, d] (any strides) to the attention's inputs
     Q [B, H, N, d], K, V [B, Hkv, N, d]: per-head norm, rotation and transposition in one pass.
     v and V may be None together."""
-    _here(q, k, v, Q, K, V, *r.tensors)
-    _check_prep_tensors(p, r)
+    import torch
+    dev, t = torch.cuda.current_device(), _storage(p)
+    B, H, Hkv, N, d = p.B, p.H, p.Hkv, p.N, p.d
+    _check_prep_tensors(p, r, dev)
     st = DmaPrepStrides()
-    qp = _rows_ptr("q", q, (p.B, p.N, p.H, p.d), st.q, p)
-    kp = _rows_ptr("k", k, (p.B, p.N, p.Hkv, p.d), st.k, p)
-    vp = _rows_ptr("v", v, (p.B, p.N, p.Hkv, p.d), st.v, p)
-    _shaped("Q", Q, (p.B, p.H, p.N, p.d), p)
-    _shaped("K", K, (p.B, p.Hkv, p.N, p.d), p)
-    _shaped("V", V, (p.B, p.Hkv, p.N, p.d), p)
-    check("dma_prep", load().dma_prep(ctypes.byref(p), ctypes.byref(r), ctypes.byref(st), qp, kp, vp, _ptr(Q), _ptr(K),
-                                      _ptr(V), _stream(stream)))
+    check("dma_prep", load().dma_prep(
+        p, r, st, _rows("q", q, (B, N, H, d), t, dev, st.q), _rows("k", k, (B, N, Hkv, d), t, dev, st.k),
+        _rows("v", v, (B, N, Hkv, d), t, dev, st.v), _dense("Q", Q, (B, H, N, d), t, dev),
+        _dense("K", K, (B, Hkv, N, d), t, dev), _dense("V", V, (B, Hkv, N, d), t, dev), _stream_on(stream, dev)))
 
 
 def prep_workspace_size(p, r) -> int:
     n = ctypes.c_size_t(0)
-    check("dma_prep_workspace_size", load().dma_prep_workspace_size(ctypes.byref(p), ctypes.byref(r), ctypes.byref(n)))
+    check("dma_prep_workspace_size", load().dma_prep_workspace_size(p, r, n))
     return int(n.value)
 
 
@@ -265,20 +284,24 @@ def prep_bwd(p, r, q, k, dQ, dK, dV, dV_gate, dq, dk, dv, dq_weight, dk_weight, 
     """Gradients of prep's inputs from those of its outputs: dq, dk, dv are written at their own
     strides ([B, N, heads, d]), dV_gate (float32, or None) is added to dV, dq_weight and dk_weight are
     float32 [d] (None: not wanted); q, k as in prep (None where there is no weight)."""
-    _here(q, k, dQ, dK, dV, dV_gate, dq, dk, dv, dq_weight, dk_weight, workspace, *r.tensors)
-    _check_prep_tensors(p, r)
+    import torch
+    dev, t, f = torch.cuda.current_device(), _storage(p), torch.float32
+    B, H, Hkv, N, d = p.B, p.H, p.Hkv, p.N, p.d
+    _check_prep_tensors(p, r, dev)
     st, gst = DmaPrepStrides(), DmaPrepStrides()
-    sq, sk = (p.B, p.N, p.H, p.d), (p.B, p.N, p.Hkv, p.d)
-    ptrs = [_rows_ptr("dq", dq, sq, gst.q, p), _rows_ptr("dk", dk, sk, gst.k, p), _rows_ptr("dv", dv, sk, gst.v, p)]
-    qp, kp = _rows_ptr("q", q, sq, st.q, p), _rows_ptr("k", k, sk, st.k, p)
-    _shaped("dQ", dQ, (p.B, p.H, p.N, p.d), p)
-    for name, t, like in (("dK", dK, p), ("dV", dV, p), ("dV_gate", dV_gate, None)):
-        _shaped(name, t, (p.B, p.Hkv, p.N, p.d), like)
-    _shaped("dq_weight", dq_weight, (p.d,))
-    _shaped("dk_weight", dk_weight, (p.d,))
-    check("dma_prep_bwd", load().dma_prep_bwd(ctypes.byref(p), ctypes.byref(r), ctypes.byref(st), ctypes.byref(gst), qp, kp,
-                                              _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(dV_gate), *ptrs, _ptr(dq_weight),
-                                              _ptr(dk_weight), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+    sq, sk, hq, hk = (B, N, H, d), (B, N, Hkv, d), (B, H, N, d), (B, Hkv, N, d)
+    check("dma_prep_bwd", load().dma_prep_bwd(
+        p, r, st, gst, _rows("q", q, sq, t, dev, st.q), _rows("k", k, sk, t, dev, st.k), _dense("dQ", dQ, hq, t, dev),
+        _dense("dK", dK, hk, t, dev), _dense("dV", dV, hk, t, dev), _dense("dV_gate", dV_gate, hk, f, dev),
+        _rows("dq", dq, sq, t, dev, gst.q), _rows("dk", dk, sk, t, dev, gst.k), _rows("dv", dv, sk, t, dev, gst.v),
+        _dense("dq_weight", dq_weight, (d,), f, dev), _dense("dk_weight", dk_weight, (d,), f, dev),
+        _workspace(workspace, dev), _nbytes(workspace), _stream_on(stream, dev)))
+
+
+def _workspace(ws, dev):
+    if ws is not None and ws.get_device() != dev:
+        raise ValueError(f"the workspace must be on the current device (cuda:{dev}), not {ws.device}")
+    return _ptr(ws)
 
 
 # ---------------------------------------------------------------- paged cache
@@ -289,18 +312,15 @@ def make_pages(p, K, V, delta, table, lens, prefix=0) -> DmaPages:
     result keeps alive; they may be written to between calls).  prefix: leading positions that every
     sequence shares, a multiple of the page length."""
     import torch
-    if K.dim() != 4:
-        raise ValueError("K must be [n_pages, Hkv, page, d]")
-    n, _, page, _ = K.shape
-    _here(K, V, delta, table, lens)
-    _shaped("K", K, (n, p.Hkv, page, p.d), p)
-    _shaped("V", V, (n, p.Hkv, page, p.d), p)
-    _shaped("delta", delta, (n, p.H, page))
-    if table.dim() != 2 or table.shape[0] != p.B or tuple(lens.shape) != (p.B,):
-        raise ValueError(f"table must be [{p.B}, max_pages] and lens [{p.B}]")
-    if table.dtype != torch.int32 or lens.dtype != torch.int32:
-        raise ValueError("table and lens must be torch.int32")
-    c = DmaPages(K=_ptr(K), V=_ptr(V), delta=_ptr(delta), table=_ptr(table), lens=_ptr(lens), n_pages=n, page=page,
+    if K.dim() != 4 or table.dim() != 2:
+        raise ValueError("K must be [n_pages, Hkv, page, d] and table [B, max_pages]")
+    dev, t = torch.cuda.current_device(), _storage(p)
+    n, page = K.shape[0], K.shape[2]
+    rows = (n, p.Hkv, page, p.d)
+    c = DmaPages(K=_dense("K", K, rows, t, dev), V=_dense("V", V, rows, t, dev),
+                 delta=_dense("delta", delta, (n, p.H, page), torch.float32, dev),
+                 table=_dense("table", table, (p.B, table.shape[1]), torch.int32, dev),
+                 lens=_dense("lens", lens, (p.B,), torch.int32, dev), n_pages=n, page=page,
                  max_pages=table.shape[1], prefix=int(prefix))
     c.tensors = (K, V, delta, table, lens)
     return c
@@ -308,7 +328,7 @@ def make_pages(p, K, V, delta, table, lens, prefix=0) -> DmaPages:
 
 def paged_layout(p, c) -> DmaPagedLayout:
     lay = DmaPagedLayout()
-    check("dma_paged_layout", load().dma_paged_layout(ctypes.byref(p), ctypes.byref(c), ctypes.byref(lay)))
+    check("dma_paged_layout", load().dma_paged_layout(p, c, lay))
     return lay
 
 
@@ -317,39 +337,35 @@ def paged_append(p, c, r, q, k, v, Delta, A, Q, workspace, starts=None, stream=N
     as the last positions of c.lens: K normed and rotated, V, the gate values; Q [T, H, d] receives the
     normed and rotated queries (q and Q may be None together).  starts: device int32 [B + 1], the
     sequences' token ranges; None: one token each."""
-    _here(q, k, v, Delta, A, Q, workspace, starts)
-    T = k.shape[0]
+    import torch
+    dev, t, f = torch.cuda.current_device(), _storage(p), torch.float32
+    T, H, Hkv, d = k.shape[0], p.H, p.Hkv, p.d
+    _check_prep_tensors(p, r, dev)
     st = DmaPrepStrides()
-    qp = _rows_ptr("q", q, (T, p.H, p.d), st.q, p)
-    kp = _rows_ptr("k", k, (T, p.Hkv, p.d), st.k, p)
-    vp = _rows_ptr("v", v, (T, p.Hkv, p.d), st.v, p)
-    _shaped("Q", Q, (T, p.H, p.d), p)
-    _shaped("Delta", Delta, (p.Hkv * p.d, p.H), p)
-    _shaped("A", A, (p.H,))
-    _check_prep_tensors(p, r)
-    if starts is not None and (tuple(starts.shape) != (p.B + 1,) or str(starts.dtype) != "torch.int32"):
-        raise ValueError(f"starts must be torch.int32 [{p.B + 1}]")
-    check("dma_paged_append", load().dma_paged_append(ctypes.byref(p), ctypes.byref(c), ctypes.byref(r),
-                                                      ctypes.byref(st), T, _ptr(starts), qp, kp, vp, _ptr(Delta),
-                                                      _ptr(A), _ptr(Q), _ptr(workspace), _nbytes(workspace),
-                                                      _stream(stream)))
+    check("dma_paged_append", load().dma_paged_append(
+        p, c, r, st, T, _dense("starts", starts, (p.B + 1,), torch.int32, dev),
+        _rows("q", q, (T, H, d), t, dev, st.q), _rows("k", k, (T, Hkv, d), t, dev, st.k),
+        _rows("v", v, (T, Hkv, d), t, dev, st.v), _dense("Delta", Delta, (Hkv * d, H), t, dev),
+        _dense("A", A, (H,), f, dev), _dense("Q", Q, (T, H, d), t, dev), _workspace(workspace, dev),
+        _nbytes(workspace), _stream_on(stream, dev)))
 
 
 def paged_topk(p, c, workspace, stream=None):
     """Selection of every (sequence, head) over its cache, into the workspace."""
-    _here(workspace)
-    check("dma_paged_topk", load().dma_paged_topk(ctypes.byref(p), ctypes.byref(c), _ptr(workspace),
-                                                  _nbytes(workspace), _stream(stream)))
+    import torch
+    dev = torch.cuda.current_device()
+    check("dma_paged_topk", load().dma_paged_topk(p, c, _workspace(workspace, dev), _nbytes(workspace),
+                                                  _stream_on(stream, dev)))
 
 
 def paged_attn(p, c, Q, workspace, O, LSE, stream=None):
     """Attention of one query [B, H, d] for each sequence over the keys paged_topk selected."""
-    _here(Q, workspace, O, LSE)
-    _shaped("Q", Q, (p.B, p.H, p.d), p)
-    _shaped("O", O, (p.B, p.H, p.d), p)
-    _shaped("LSE", LSE, (p.B, p.H))
-    check("dma_paged_attn", load().dma_paged_attn(ctypes.byref(p), ctypes.byref(c), _ptr(Q), _ptr(workspace),
-                                                  _nbytes(workspace), _ptr(O), _ptr(LSE), _stream(stream)))
+    import torch
+    dev, t = torch.cuda.current_device(), _storage(p)
+    shape = (p.B, p.H, p.d)
+    check("dma_paged_attn", load().dma_paged_attn(
+        p, c, _dense("Q", Q, shape, t, dev), _workspace(workspace, dev), _nbytes(workspace),
+        _dense("O", O, shape, t, dev), _dense("LSE", LSE, (p.B, p.H), torch.float32, dev), _stream_on(stream, dev)))
 
 
 # ---------------------------------------------------------------- convenience (torch allocation)

@@ -3,7 +3,7 @@
 // normed and rotated.
 //
 // Two kernels that run side by side: the gate's product (the values of 16 tokens against Delta, tensor
-// cores for bf16) and the rows (a warp per token, as in prep.cu).  The second is launched as a
+// cores for bf16) and the walk over the rows (rows.cuh, as in prep.cu).  The second is launched as a
 // programmatic dependent of the first, which lets it go at once; it waits for the first only before it
 // ends, so that whatever follows in the stream finds both done.
 #include "rows.cuh"
@@ -50,74 +50,33 @@ DMA_DEVINL Place place_of(const PagedPlan& P, const PagedAppendArgs& a, int t, i
 
 // ---------------------------------------------------------------- rows
 
-constexpr int kArThreads = 256;
-constexpr int kArWarps = kArThreads / 32;
-
-template <typename T, int D, int U>
-__global__ void __launch_bounds__(kArThreads)
-paged_rows_kernel(PagedPlan P, PagedAppendArgs a, int wt, int32_t* status) {
-  constexpr int L = D / 8, RPW = 32 / L;
-  __shared__ float2 tab[kArWarps][D / 2];
-  __shared__ Place place[kArWarps];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int tpb = kArWarps / wt, half = a.r.rot >> 1;
-  const int t0 = blockIdx.x * tpb;
-  if (warp < tpb) {
-    Place pl = {0, -1, 0, 0};
-    if (t0 + warp < a.T) pl = place_of(P, a, t0 + warp, status);
-    if (lane == 0) place[warp] = pl;
-    if (pl.pos >= 0)
-      for (int k = lane; k < half; k += 32) tab[warp][k] = turn_of(pl.pos, __ldg(a.r.inv_freq + k));
+// Keys and values to their slots, queries to Q [T, H, D].
+struct SlotDest {
+  struct Token {
+    int position;
+    unsigned tok;
+    size_t slot;   // of head 0, in rows
+  };
+  PagedPlan P;
+  PagedAppendArgs a;
+  int32_t* status;
+  int size;
+  DMA_DEVINL bool enter(unsigned tok, unsigned, unsigned, Token& t) const {
+    const Place pl = place_of(P, a, (int)tok, status);
+    t.tok = tok;
+    t.position = pl.pos;
+    t.slot = ((size_t)pl.page * P.Hkv << P.page_shift) + pl.slot;
+    return pl.pos >= 0;
   }
-  __syncthreads();
-  const Place pl = place[warp / wt];
-  if (pl.pos >= 0) {
-    const long long t = t0 + warp / wt;
-    const int grp = lane / L, e = (lane % L) * 8, page = 1 << P.page_shift;
-    LaneTurn turn;
-    lane_turn<L>(turn, tab[warp / wt], a.r.rot, a.r.interleaved != 0, lane);
-    const size_t slot = ((size_t)pl.page * P.Hkv * page + pl.slot) * D + e;   // of head 0
-#pragma unroll
-    for (int part = 0; part < 3; ++part) {   // keys, values, queries
-      if (part == 2 && a.q == nullptr) continue;
-      const int heads = part == 2 ? P.H : P.Hkv;
-      const int64_t* st = part == 0 ? a.st.k : part == 1 ? a.st.v : a.st.q;
-      const T* src = (const T*)(part == 0 ? a.k : part == 1 ? a.v : a.q) + t * st[1] + e;
-      T* dst = part == 0 ? (T*)P.K + slot : part == 1 ? (T*)P.V + slot : (T*)a.Q + (size_t)t * P.H * D + e;
-      const size_t dh = part == 2 ? (size_t)D : (size_t)page * D;
-      const long long sh = st[2];
-      const T* wp = (const T*)(part == 0 ? a.r.k_weight : part == 2 ? a.r.q_weight : nullptr);
-      float g[8];
-      if (wp) widen8(load_raw8(wp + e), g);
-      for (int h0 = (warp % wt) * RPW * U; h0 < heads; h0 += wt * RPW * U) {
-        Raw8<T> raw[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) raw[u] = load_raw8(src + min(h0 + u * RPW + grp, heads - 1) * sh);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int h = h0 + u * RPW + grp;
-          if (part == 1) {
-            if (h < heads) store_raw8(dst + h * dh, raw[u]);
-            continue;
-          }
-          float y[8];
-          widen8(raw[u], y);
-          if (wp) {
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
-            const float r = rsqrtf(row_sum<L>(ss) * (1.f / D) + a.r.eps);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] *= r * g[i];
-          }
-          rotate8<false>(y, turn, a.r.interleaved != 0);
-          if (h < heads) store8(dst + h * dh, y);
-        }
-      }
-    }
+  DMA_DEVINL void* row(int part, const Token& t) const {
+    if (part == 0) return (char*)a.Q + (size_t)t.tok * P.H * P.d * size;
+    return (part == 1 ? P.K : P.V) + t.slot * P.d * size;
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // the gate kernel in front is done too
-}
+  DMA_DEVINL size_t step(int part) const { return part == 0 ? (size_t)P.d : (size_t)P.d << P.page_shift; }
+  DMA_DEVINL void finish() const {
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the gate kernel in front is done too
+  }
+};
 
 // ---------------------------------------------------------------- gate, tensor cores
 
@@ -308,20 +267,26 @@ cudaError_t launch_gate(const PagedPlan& P, const PagedAppendArgs& a, int32_t* s
 
 template <typename T, int D>
 cudaError_t launch_rows(const PagedPlan& P, const PagedAppendArgs& a, int32_t* status, cudaStream_t s) {
-  const int sms = sm_count();
-  int wt = 1;   // warps that share a token: enough to give every SM a block
-  while (wt < kArWarps && (long long)a.T * wt < (long long)sms * kArWarps) wt *= 2;
-  const int tpb = kArWarps / wt;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((a.T + tpb - 1) / tpb);
-  cfg.blockDim = dim3(kArThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_rows_kernel<T, D, 4>, P, a, wt, status);
+  PrepArgs w = {};
+  w.inv_freq = a.r.inv_freq;
+  w.weight[0] = a.r.q_weight;
+  w.weight[1] = a.r.k_weight;
+  w.in[0] = a.q; w.in[1] = a.k; w.in[2] = a.v;
+  w.out[0] = a.Q; w.out[1] = P.K; w.out[2] = P.V;
+  for (int i = 1; i < 3; ++i) {
+    w.stride[0][i] = a.st.q[i];
+    w.stride[1][i] = a.st.k[i];
+    w.stride[2][i] = a.st.v[i];
+  }
+  w.eps = a.r.eps;
+  w.B = 1; w.H = P.H; w.Hkv = P.Hkv; w.N = a.T; w.rot = a.r.rot;
+  w.inter = a.r.interleaved != 0;
+  SlotDest d = {};
+  d.P = P;
+  d.a = a;
+  d.status = status;
+  d.size = (int)sizeof(T);
+  return launch_row_walk<T, D>(w, d, true, s);
 }
 
 }  // namespace

@@ -15,257 +15,214 @@
 namespace dma {
 namespace {
 
-constexpr int kPrThreads = 256;
-constexpr int kPrWarps = kPrThreads / 32;
+// Dense outputs [B, heads, N, D].
+struct DenseDest {
+  struct Token {
+    int position;
+    unsigned b, n;
+  };
+  void* out[3];
+  const int32_t* positions;
+  unsigned N;
+  int H, Hkv, D, size, first;
+  DMA_DEVINL bool enter(unsigned tok, unsigned b, unsigned n, Token& t) const {
+    t.b = b;
+    t.n = n;
+    t.position = positions ? __ldg(positions + tok) : first + (int)t.n;
+    return true;
+  }
+  DMA_DEVINL void* row(int part, const Token& t) const {
+    return (char*)out[part] + (((size_t)t.b * (part == 0 ? H : Hkv)) * N + t.n) * D * size;
+  }
+  DMA_DEVINL size_t step(int) const { return (size_t)N * D; }
+  DMA_DEVINL void finish() const {}
+};
 
-// A warp works on one token at a time, its D / 8-lane groups on neighbouring heads; wt = 1, 2, 4 or 8
-// warps of a block share a token's heads (many for few tokens, so that the heads of a single token
-// spread over the block).  The angles of a block's tokens are computed once into shared memory and
-// kept in registers over the token's heads.
-template <typename T, int D, int U>
-__global__ void __launch_bounds__(kPrThreads)
-prep_fwd_kernel(PrepArgs a, int wt) {
-  constexpr int L = D / 8, RPW = 32 / L;   // lanes of a row, rows of a warp
-  __shared__ float2 tab[kPrWarps][D / 2];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int tpb = kPrWarps / wt;
-  const long long t0 = (long long)blockIdx.x * tpb, nt = (long long)a.B * a.N;
-  const int half = a.rot >> 1;
-  for (int u = tid; u < tpb * half; u += kPrThreads) {
-    const int tt = u / half, k = u - tt * half;
-    const long long t = t0 + tt;
-    if (t < nt) {
-      const int pos = a.positions ? a.positions[t] : a.first + (int)(t % a.N);
-      tab[tt][k] = turn_of(pos, __ldg(a.inv_freq + k));
-    }
-  }
-  __syncthreads();
-  const long long t = t0 + warp / wt;
-  if (t >= nt) return;
-  const int b = (int)(t / a.N), n = (int)(t - (long long)b * a.N);
-  const int grp = lane / L, e = (lane % L) * 8;
-  LaneTurn turn;
-  lane_turn<L>(turn, tab[warp / wt], a.rot, a.inter, lane);
-  const T* src[3];
-  long long hs[3];
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    src[i] = (const T*)a.in[i] + b * a.stride[i][0] + n * a.stride[i][1] + e;
-    hs[i] = a.stride[i][2];
-  }
-  // queries, then keys, then values: U rows of loads in flight in each lane
-#pragma unroll 1
-  for (int part = 0; part < 3; ++part) {
-    if (a.out[part] == nullptr) continue;
-    const int heads = part == 0 ? a.H : a.Hkv;
-    T* dst = (T*)a.out[part] + ((long long)b * heads * a.N + n) * D + e;
-    const T* wp = part < 2 ? (const T*)a.weight[part] : nullptr;
-    float g[8];
-    if (wp) widen8(load_raw8(wp + e), g);
-    const T* sp = src[part];
-    const long long sh = hs[part], dh = (long long)a.N * D;
-    for (int h0 = (warp % wt) * RPW * U; h0 < heads; h0 += wt * RPW * U) {
-      Raw8<T> raw[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = min(h0 + u * RPW + grp, heads - 1);   // past the end: the last row again, not stored
-        raw[u] = load_raw8(sp + h * sh);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * RPW + grp;
-        if (part == 2) {
-          if (h < heads) store_raw8(dst + h * dh, raw[u]);
-          continue;
-        }
-        float y[8];
-        widen8(raw[u], y);
-        if (wp) {
-          float ss = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
-          const float r = rsqrtf(row_sum<L>(ss) * (1.f / D) + a.eps);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] *= r * g[i];
-        }
-        rotate8<false>(y, turn, a.inter);
-        if (h < heads) store8(dst + h * dh, y);
-      }
-    }
-  }
-}
+template <typename T> constexpr int bwd_rows() { return sizeof(T) == 2 ? 2 : 1; }
+// a row's gradient, and its input or (values) the gate's share
+template <typename T> using BwdRing = RowRing<sizeof(T) == 2 ? 3 : 4, bwd_rows<T>(), 4>;
 
-// Blocks walk over the tokens in a fixed order, so the partial sums of the weights' gradients (float32
+// Warps walk over the tokens in a fixed order, so the partial sums of the weights' gradients (float32
 // within a lane, at most a few thousand rows each) do not depend on scheduling.
-template <typename T, int D, int U>
-__global__ void __launch_bounds__(kPrThreads)
-prep_bwd_kernel(PrepArgs a, int wt) {
-  constexpr int L = D / 8, RPW = 32 / L;
-  __shared__ float2 tab[kPrWarps][D / 2];
-  __shared__ float red[kPrWarps * RPW][D];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int tpb = kPrWarps / wt;
-  const long long nt = (long long)a.B * a.N;
-  const int half = a.rot >> 1;
-  const int grp = lane / L, e = (lane % L) * 8;
-  float gw[2][8];   // this lane's share of the weights' gradients
+template <typename T, int D, bool INTER>
+__global__ void __launch_bounds__(kRwThreads, 2)
+prep_bwd_kernel(const __grid_constant__ PrepArgs a, int wt) {
+  constexpr int L = D / 8, RPW = 32 / L, U = bwd_rows<T>(), SECOND = sizeof(T) / 2;
+  using Ring = BwdRing<T>;
+  extern __shared__ __align__(128) unsigned char ring_smem[];
+  __shared__ __align__(16) float2 tab[kRwWarps][D / 2 + kTabPad];
+  __shared__ uint64_t rate[D / 2];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grp = lane / L, e = (lane % L) * 8;
+  const bool upper = e >= a.rot >> 1;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int k = tid; k < a.rot >> 1; k += kRwThreads) rate[k] = turn_rate(__ldg(a.inv_freq + k));
+  if (lane < kTabPad) tab[warp][D / 2 + lane] = make_float2(1.f, 0.f);
+  __syncthreads();
+  auto send = [&](const Walk& at, unsigned char* place) {
+    const int part = at.part(), h = at.within(part) * (RPW * U) + grp, heads = part == 0 ? a.H : a.Hkv, left = heads - h;
+    const size_t dense = (((size_t)at.b * heads + h) * at.N + at.n) * D + e, step = (size_t)RPW * at.N * D;
+    const T* base = (const T*)a.grad[part];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) gw[0][i] = gw[1][i] = 0.f;
-  for (long long t0 = (long long)blockIdx.x * tpb; t0 < nt; t0 += (long long)gridDim.x * tpb) {
-    __syncthreads();   // the angles of the last round are no longer read
-    for (int u = tid; u < tpb * half; u += kPrThreads) {
-      const int tt = u / half, k = u - tt * half;
-      const long long t = t0 + tt;
-      if (t < nt) {
-        const int pos = a.positions ? a.positions[t] : a.first + (int)(t % a.N);
-        tab[tt][k] = turn_of(pos, __ldg(a.inv_freq + k));
-      }
+    for (int u = 0; u < U; ++u)
+      Ring::copy(place + u * Ring::kRow, 0, u * RPW < left ? base + dense + u * step : base, u * RPW < left);
+    if (part == 2) {
+      if (a.dv_gate == nullptr) return;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        Ring::copy(place + u * Ring::kRow, SECOND, u * RPW < left ? a.dv_gate + dense + u * step : a.dv_gate,
+                   u * RPW < left);
+    } else if (a.weight[part] != nullptr) {
+      const long long sh = a.stride[part][2];
+      const T* x = (const T*)a.in[part];
+      const T* src = x + at.b * a.stride[part][0] + at.n * a.stride[part][1] + h * sh + e;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        Ring::copy(place + u * Ring::kRow, SECOND, u * RPW < left ? src + u * RPW * sh : x, u * RPW < left);
     }
-    __syncthreads();
-    const long long t = t0 + warp / wt;
-    if (t >= nt) continue;
-    const int b = (int)(t / a.N), n = (int)(t - (long long)b * a.N);
-    LaneTurn turn;
-    lane_turn<L>(turn, tab[warp / wt], a.rot, a.inter, lane);
+  };
+  uint64_t gw[2][4];   // this lane's share of the weights' gradients
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      const int heads = part == 0 ? a.H : a.Hkv;
-      const T* dy = (const T*)a.grad[part] + ((long long)b * heads * a.N + n) * D + e;
-      const long long dh = (long long)a.N * D, sh = a.stride[part][2], gh = a.gstride[part][2];
-      const T* xp = (const T*)a.in[part] + b * a.stride[part][0] + n * a.stride[part][1] + e;
-      T* dx = (T*)a.out[part] + b * a.gstride[part][0] + n * a.gstride[part][1] + e;
-      const T* wp = (const T*)a.weight[part];
-      float g[8];
-      if (wp) widen8(load_raw8(wp + e), g);
-      for (int h0 = (warp % wt) * RPW * U; h0 < heads; h0 += wt * RPW * U) {
-        Raw8<T> rg[U], rx[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int h = min(h0 + u * RPW + grp, heads - 1);
-          rg[u] = load_raw8(dy + h * dh);
-          if (wp) rx[u] = load_raw8(xp + h * sh);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int h = h0 + u * RPW + grp;
-          float y[8];
-          widen8(rg[u], y);
-          rotate8<true>(y, turn, a.inter);
-          if (wp) {
-            float x[8], ss = 0.f, dot = 0.f;
-            widen8(rx[u], x);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              ss = fmaf(x[i], x[i], ss);
-              dot = fmaf(x[i] * g[i], y[i], dot);
-            }
-            const float r = rsqrtf(row_sum<L>(ss) * (1.f / D) + a.eps);
-            const float k = row_sum<L>(dot) * (1.f / D) * r * r;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              if (h < heads) gw[part][i] = fmaf(y[i], x[i] * r, gw[part][i]);
-              y[i] = r * fmaf(-x[i], k, g[i] * y[i]);
-            }
-          }
-          if (h < heads) store8(dx + h * gh, y);
-        }
-      }
+  for (int i = 0; i < 4; ++i) gw[0][i] = gw[1][i] = 0;
+  LaneTurn turn;
+  const int start = lane_start<D>(turn, a.rot, INTER, lane);
+  unsigned have = 0xffffffffu;
+  auto work = [&](const Walk& at, const unsigned char* place) {
+    if (have != at.tok) {
+      have = at.tok;
+      token_table(rate, a.rot >> 1, a.positions ? __ldg(a.positions + at.tok) : a.first + (int)at.n, tab[warp]);
+      lane_turn<INTER>(turn, tab[warp], start, upper, true);
     }
-    if (a.out[2]) {
-      const T* dv = (const T*)a.grad[2] + ((long long)b * a.Hkv * a.N + n) * D + e;
-      const float* dvg = a.dv_gate ? a.dv_gate + ((long long)b * a.Hkv * a.N + n) * D + e : nullptr;
-      T* out = (T*)a.out[2] + b * a.gstride[2][0] + n * a.gstride[2][1] + e;
-      for (int h0 = (warp % wt) * RPW * U; h0 < a.Hkv; h0 += wt * RPW * U) {
-        Raw8<T> rv[U];
-        Raw8<float> rg[U];
+    const int part = at.part(), h = at.within(part) * (RPW * U) + grp, left = (part == 0 ? a.H : a.Hkv) - h;
+    const long long sh = a.gstride[part][2];
+    T* dst = (T*)a.out[part] + at.b * a.gstride[part][0] + at.n * a.gstride[part][1] + h * sh + e;
+    if (part == 2) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const long long h = min(h0 + u * RPW + grp, a.Hkv - 1);
-          rv[u] = load_raw8(dv + h * a.N * D);
-          if (dvg) rg[u] = load_raw8(dvg + h * a.N * D);
-        }
+      for (int u = 0; u < U; ++u) {
+        if (u * RPW < left) {
+          if (a.dv_gate != nullptr) {
+            Pair8 v = pairs8(Ring::template read<T>(place + u * Ring::kRow, 0));
+            const Pair8 w = pairs8(Ring::template read<float>(place + u * Ring::kRow, SECOND));
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int h = h0 + u * RPW + grp;
-          if (h >= a.Hkv) continue;
-          if (dvg) {
-            float v[8], w[8];
-            widen8(rv[u], v);
-            widen8(rg[u], w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += w[i];
-            store8(out + h * a.gstride[2][2], v);
+            for (int i = 0; i < 4; ++i) v.v[i] = f2_add(v.v[i], w.v[i]);
+            store8(dst, v);
           } else {
-            store_raw8(out + h * a.gstride[2][2], rv[u]);
+            store_raw8(dst, Ring::template read<T>(place + u * Ring::kRow, 0));
           }
         }
+        dst += RPW * sh;
       }
+      return;
     }
-  }
-  // the block's partial sums of dg, one row of the workspace each
+    const T* wp = (const T*)a.weight[part];
+    Pair8 g;
+    if (wp != nullptr) g = pairs8(load_raw8(wp + e));
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      Pair8 y = rotate8<INTER>(pairs8(Ring::template read<T>(place + u * Ring::kRow, 0)), turn);
+      if (wp != nullptr) {
+        const Pair8 x = pairs8(Ring::template read<T>(place + u * Ring::kRow, SECOND));   // zeros past the last head
+        Pair8 gy, t;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          gy.v[i] = f2_mul(g.v[i], y.v[i]);
+          t.v[i] = f2_mul(x.v[i], y.v[i]);
+        }
+        const float rn = rsqrtf(row_dot<L>(x, x) * (1.f / D) + a.eps);
+        const float k = row_dot<L>(gy, x) * (-1.f / D) * rn * rn * rn;
+        const uint64_t rr = f2(rn, rn), kk = f2(k, k);
+        if (part == 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) gw[0][i] = f2_fma(t.v[i], rr, gw[0][i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) gw[1][i] = f2_fma(t.v[i], rr, gw[1][i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y.v[i] = f2_fma(x.v[i], kk, f2_mul(gy.v[i], rr));
+      }
+      if (u * RPW < left) store8(dst, y);
+      dst += RPW * sh;
+    }
+  };
+  Ring::run(Walk(a, RPW * U, wt), ring_smem, send, work);
+  // the block's partial sums of dg, one row of the workspace each, in the ring's place
+  float* red = reinterpret_cast<float*>(ring_smem);   // [kRwWarps * RPW][D]
+  static_assert(Ring::kBytes >= kRwWarps * RPW * D * 4, "the sums fit into the ring");
+  cp_async_wait<0>();
 #pragma unroll
   for (int part = 0; part < 2; ++part) {
     if (!a.weight[part]) continue;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) red[warp * RPW + grp][e + i] = gw[part][i];
+    for (int i = 0; i < 4; ++i)
+      f2_split(gw[part][i], red[(warp * RPW + grp) * D + e + 2 * i], red[(warp * RPW + grp) * D + e + 2 * i + 1]);
     __syncthreads();
-    for (int c = tid; c < D; c += kPrThreads) {
+    for (int c = tid; c < D; c += kRwThreads) {
       float v = 0.f;
 #pragma unroll
-      for (int q = 0; q < kPrWarps * RPW; ++q) v += red[q][c];
+      for (int q = 0; q < kRwWarps * RPW; ++q) v += red[q * D + c];
       a.part[((size_t)part * gridDim.x + blockIdx.x) * D + c] = v;
     }
   }
 }
 
-// dg[c] = sum over blocks, in double precision: at most kPrepMaxBlocks terms per channel, 32 channels a block.
+// dg[c] = sum over blocks, in double precision: at most kPrepMaxBlocks terms per channel.  A block takes
+// eight channels (a 32-byte sector of every partial row), so that a thread has only a few loads to wait for.
 __global__ void __launch_bounds__(1024)
 prep_reduce_kernel(const float* __restrict__ part, float* __restrict__ dq_weight, float* __restrict__ dk_weight,
                    int n_blocks, int D) {
-  __shared__ double red[32][33];
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+  __shared__ double red[32][8];
+  const int tid = threadIdx.x, c = blockIdx.x * 8 + (tid & 7), w = tid >> 3;
   float* out = blockIdx.y == 0 ? dq_weight : dk_weight;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (out == nullptr) return;
   const float* p = part + (size_t)blockIdx.y * n_blocks * D + c;
   double v = 0.0;
-  for (int i = w; i < n_blocks; i += 32) v += (double)p[(size_t)i * D];
-  red[w][threadIdx.x & 31] = v;
+#pragma unroll 5
+  for (int i = w; i < n_blocks; i += 128) v += (double)p[(size_t)i * D];
+  v += __shfl_xor_sync(0xffffffffu, v, 8);
+  v += __shfl_xor_sync(0xffffffffu, v, 16);
+  if ((tid & 31) < 8) red[tid >> 5][tid & 7] = v;
   __syncthreads();
-  if (w == 0) {
+  if (tid < 8) {
     double s = 0.0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) s += red[i][threadIdx.x];
+    for (int i = 0; i < 32; ++i) s += red[i][tid];
     out[c] = (float)s;
   }
 }
 
-// Warps that share a token: as many as it takes to give every SM a block, 8 at most.
-int warps_per_token(long long tokens, int sms) {
-  int wt = 1;
-  while (wt < kPrWarps && tokens * wt < (long long)sms * kPrWarps) wt *= 2;
-  return wt;
-}
-
 template <typename T, int D>
 cudaError_t launch_fwd(const PrepArgs& a, cudaStream_t s) {
-  const long long tokens = (long long)a.B * a.N;
-  const int wt = warps_per_token(tokens, sm_count()), tpb = kPrWarps / wt;
-  prep_fwd_kernel<T, D, 4><<<(unsigned)((tokens + tpb - 1) / tpb), kPrThreads, 0, s>>>(a, wt);
-  return cudaGetLastError();
+  DenseDest d = {};
+  for (int i = 0; i < 3; ++i) d.out[i] = a.out[i];
+  d.positions = a.positions;
+  d.N = (unsigned)a.N;
+  d.H = a.H; d.Hkv = a.Hkv; d.D = D; d.size = (int)sizeof(T); d.first = a.first;
+  return launch_row_walk<T, D>(a, d, false, s);
 }
 
 template <typename T, int D>
 cudaError_t launch_bwd(const PrepArgs& a, float* dqw, float* dkw, cudaStream_t s) {
-  const long long tokens = (long long)a.B * a.N;
-  const int wt = warps_per_token(tokens, sm_count()), tpb = kPrWarps / wt;
-  long long blocks = (tokens + tpb - 1) / tpb;
+  int wt;
+  int blocks = walk_blocks((long long)a.B * a.N, 2, &wt);
   if (blocks > kPrepMaxBlocks) blocks = kPrepMaxBlocks;
-  prep_bwd_kernel<T, D, 2><<<(unsigned)blocks, kPrThreads, 0, s>>>(a, wt);
-  cudaError_t e = cudaGetLastError();
+  auto kernel = a.inter ? prep_bwd_kernel<T, D, true> : prep_bwd_kernel<T, D, false>;
+  cudaError_t e = ensure_smem_limit(kernel, BwdRing<T>::kBytes);
+  if (e != cudaSuccess) return e;
+  kernel<<<blocks, kRwThreads, BwdRing<T>::kBytes, s>>>(a, wt);
+  e = cudaGetLastError();
   if (e != cudaSuccess || (dqw == nullptr && dkw == nullptr)) return e;
-  prep_reduce_kernel<<<dim3(D / 32, 2), 1024, 0, s>>>(a.part, dqw, dkw, (int)blocks, D);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(D / 8, 2);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prep_reduce_kernel, (const float*)a.part, dqw, dkw, blocks, D);
 }
 
 }  // namespace
@@ -309,7 +266,8 @@ dma_status_t prep_args(const dma_params_t* p, const dma_prep_t* r, PrepArgs* a) 
   if (p->Nq != p->N || p->H % p->Hkv != 0) return DMA_ERR_INVALID_ARG;
   if (p->dtype != DMA_BF16 && p->dtype != DMA_F32) return DMA_ERR_INVALID_ARG;
   if (p->d != 64 && p->d != 128) return DMA_ERR_UNSUPPORTED;
-  if ((int64_t)p->B * p->H > 65535 || p->N > (1 << 24)) return DMA_ERR_UNSUPPORTED;
+  if ((int64_t)p->B * p->H > 65535 || p->N > (1 << 24) || (int64_t)p->B * p->N >= ((int64_t)1 << 31))
+    return DMA_ERR_UNSUPPORTED;
   dma_status_t st = check_prep(r, p->d);
   if (st != DMA_OK) return st;
   memset(a, 0, sizeof(*a));
