@@ -19,22 +19,21 @@ struct Place {
   int page, slot;
 };
 
-// Sequence and slot of token t; every lane of the warp calls it with the same t < T.
+// Sequence and slot of token t < T (each lane its own).
 DMA_DEVINL Place place_of(const PagedPlan& P, const PagedAppendArgs& a, int t, int32_t* status) {
-  const int lane = threadIdx.x & 31;
   int seq = t, first = t, n = 1;
   if (a.starts != nullptr) {
-    // number of sequences that end at or before t
-    seq = 0;
-    for (int i0 = 1; i0 <= P.B; i0 += 32) {
-      const int i = i0 + lane;
-      const bool before = i <= P.B && __ldg(a.starts + i) <= t;
-      seq += __popc(__ballot_sync(0xffffffffu, before));
+    // the sequence before the first that starts behind t; none: padding in front of them all, or behind
+    int lo = 0, hi = P.B + 1;   // starts[i] <= t for i < lo, > t for i >= hi
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(a.starts + mid) <= t) lo = mid + 1;
+      else hi = mid;
     }
-    if (seq >= P.B) return {0, -1, 0, 0};   // padding behind the last sequence
+    seq = lo - 1;
+    if (seq < 0 || seq >= P.B) return {0, -1, 0, 0};
     first = __ldg(a.starts + seq);
     n = __ldg(a.starts + seq + 1) - first;
-    if (t < first) return {0, -1, 0, 0};    // padding in front of the first one
   }
   const int len = __ldg(P.lens + seq);
   if (len <= 0) return {seq, -1, 0, 0};
@@ -42,7 +41,7 @@ DMA_DEVINL Place place_of(const PagedPlan& P, const PagedAppendArgs& a, int t, i
   int page = -1;
   if (pos >= 0 && pos < len && len <= P.N) page = __ldg(P.table + (size_t)seq * P.max_pages + (pos >> P.page_shift));
   if (page < 0 || page >= P.n_pages) {
-    if (lane == 0) atomicOr(status, kPagedErr);
+    atomicOr(status, kPagedErr);
     return {seq, -1, 0, 0};
   }
   return {seq, pos, page, pos & ((1 << P.page_shift) - 1)};
@@ -50,23 +49,36 @@ DMA_DEVINL Place place_of(const PagedPlan& P, const PagedAppendArgs& a, int t, i
 
 // ---------------------------------------------------------------- rows
 
-// Keys and values to their slots, queries to Q [T, H, D].
+// Keys and values to their slots, queries to Q [T, H, D].  A warp looks up the places of its next 32 tokens
+// together, a token a lane: the lookups' three or more dependent reads are then paid once.
 struct SlotDest {
   struct Token {
     int position;
     unsigned tok;
-    size_t slot;   // of head 0, in rows
+    size_t slot;        // of head 0, in rows
+    int looked_up = 0;  // tokens of the batch of 32 already entered
+    int pos, page;      // this lane's token of the batch
   };
   PagedPlan P;
   PagedAppendArgs a;
   int32_t* status;
   int size;
-  DMA_DEVINL bool enter(unsigned tok, unsigned, unsigned, Token& t) const {
-    const Place pl = place_of(P, a, (int)tok, status);
-    t.tok = tok;
-    t.position = pl.pos;
-    t.slot = ((size_t)pl.page * P.Hkv << P.page_shift) + pl.slot;
-    return pl.pos >= 0;
+  DMA_DEVINL bool enter(const Walk& at, Token& t) const {
+    const int i = t.looked_up & 31;
+    if (i == 0) {
+      const unsigned mine = at.tok + (threadIdx.x & 31) * at.step;
+      Place pl = {0, -1, 0, 0};
+      if (mine < at.tokens && mine >= at.tok) pl = place_of(P, a, (int)mine, status);
+      __syncwarp();
+      t.pos = pl.pos;
+      t.page = pl.page;
+    }
+    ++t.looked_up;
+    t.tok = at.tok;
+    t.position = __shfl_sync(0xffffffffu, t.pos, i);
+    const int page = __shfl_sync(0xffffffffu, t.page, i);
+    t.slot = ((size_t)page * P.Hkv << P.page_shift) + (t.position & ((1 << P.page_shift) - 1));
+    return t.position >= 0;
   }
   DMA_DEVINL void* row(int part, const Token& t) const {
     if (part == 0) return (char*)a.Q + (size_t)t.tok * P.H * P.d * size;
@@ -87,11 +99,11 @@ constexpr int kAgWarps = kAgThreads / 32;
 // Offset of (token's page, head 0, slot) in the delta pages of the CTA's tokens; -1: none.
 DMA_DEVINL void gate_places(const PagedPlan& P, const PagedAppendArgs& a, int t0, int n, long long* where,
                             int32_t* status) {
-  for (int i = threadIdx.x >> 5; i < n; i += kAgWarps) {
+  const int i = threadIdx.x;
+  if (i < n) {
     Place pl = {0, -1, 0, 0};
     if (t0 + i < a.T) pl = place_of(P, a, t0 + i, status);
-    if ((threadIdx.x & 31) == 0)
-      where[i] = pl.pos < 0 ? -1 : ((long long)pl.page * P.H << P.page_shift) + pl.slot;
+    where[i] = pl.pos < 0 ? -1 : ((long long)pl.page * P.H << P.page_shift) + pl.slot;
   }
 }
 

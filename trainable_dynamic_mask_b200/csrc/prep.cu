@@ -25,10 +25,10 @@ struct DenseDest {
   const int32_t* positions;
   unsigned N;
   int H, Hkv, D, size, first;
-  DMA_DEVINL bool enter(unsigned tok, unsigned b, unsigned n, Token& t) const {
-    t.b = b;
-    t.n = n;
-    t.position = positions ? __ldg(positions + tok) : first + (int)t.n;
+  DMA_DEVINL bool enter(const Walk& at, Token& t) const {
+    t.b = at.b;
+    t.n = at.n;
+    t.position = positions ? __ldg(positions + at.tok) : first + (int)t.n;
     return true;
   }
   DMA_DEVINL void* row(int part, const Token& t) const {
@@ -80,9 +80,9 @@ prep_bwd_kernel(const __grid_constant__ PrepArgs a, int wt) {
         Ring::copy(place + u * Ring::kRow, SECOND, u * RPW < left ? src + u * RPW * sh : x, u * RPW < left);
     }
   };
-  uint64_t gw[2][4];   // this lane's share of the weights' gradients
+  float gw[2][8];   // this lane's share of the weights' gradients
 #pragma unroll
-  for (int i = 0; i < 4; ++i) gw[0][i] = gw[1][i] = 0;
+  for (int i = 0; i < 8; ++i) gw[0][i] = gw[1][i] = 0.f;
   LaneTurn turn;
   const int start = lane_start<D>(turn, a.rot, INTER, lane);
   unsigned have = 0xffffffffu;
@@ -100,10 +100,10 @@ prep_bwd_kernel(const __grid_constant__ PrepArgs a, int wt) {
       for (int u = 0; u < U; ++u) {
         if (u * RPW < left) {
           if (a.dv_gate != nullptr) {
-            Pair8 v = pairs8(Ring::template read<T>(place + u * Ring::kRow, 0));
-            const Pair8 w = pairs8(Ring::template read<float>(place + u * Ring::kRow, SECOND));
+            Chan8 v = channels8(Ring::template read<T>(place + u * Ring::kRow, 0));
+            const Chan8 w = channels8(Ring::template read<float>(place + u * Ring::kRow, SECOND));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v.v[i] = f2_add(v.v[i], w.v[i]);
+            for (int i = 0; i < 8; ++i) v.v[i] += w.v[i];
             store8(dst, v);
           } else {
             store_raw8(dst, Ring::template read<T>(place + u * Ring::kRow, 0));
@@ -114,31 +114,30 @@ prep_bwd_kernel(const __grid_constant__ PrepArgs a, int wt) {
       return;
     }
     const T* wp = (const T*)a.weight[part];
-    Pair8 g;
-    if (wp != nullptr) g = pairs8(load_raw8(wp + e));
+    Chan8 g;
+    if (wp != nullptr) g = channels8(load_raw8(wp + e));
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      Pair8 y = rotate8<INTER>(pairs8(Ring::template read<T>(place + u * Ring::kRow, 0)), turn);
+      Chan8 y = rotate8<INTER>(channels8(Ring::template read<T>(place + u * Ring::kRow, 0)), turn);
       if (wp != nullptr) {
-        const Pair8 x = pairs8(Ring::template read<T>(place + u * Ring::kRow, SECOND));   // zeros past the last head
-        Pair8 gy, t;
+        const Chan8 x = channels8(Ring::template read<T>(place + u * Ring::kRow, SECOND));   // zeros past the last head
+        float t[8], dot = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          gy.v[i] = f2_mul(g.v[i], y.v[i]);
-          t.v[i] = f2_mul(x.v[i], y.v[i]);
+        for (int i = 0; i < 8; ++i) {
+          t[i] = x.v[i] * y.v[i];
+          dot = fmaf(t[i], g.v[i], dot);
         }
         const float rn = rsqrtf(row_dot<L>(x, x) * (1.f / D) + a.eps);
-        const float k = row_dot<L>(gy, x) * (-1.f / D) * rn * rn * rn;
-        const uint64_t rr = f2(rn, rn), kk = f2(k, k);
+        const float k = row_sum<L>(dot) * (-1.f / D) * rn * rn * rn;
         if (part == 0) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) gw[0][i] = f2_fma(t.v[i], rr, gw[0][i]);
+          for (int i = 0; i < 8; ++i) gw[0][i] = fmaf(t[i], rn, gw[0][i]);
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) gw[1][i] = f2_fma(t.v[i], rr, gw[1][i]);
+          for (int i = 0; i < 8; ++i) gw[1][i] = fmaf(t[i], rn, gw[1][i]);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y.v[i] = f2_fma(x.v[i], kk, f2_mul(gy.v[i], rr));
+        for (int i = 0; i < 8; ++i) y.v[i] = fmaf(x.v[i], k, y.v[i] * (g.v[i] * rn));
       }
       if (u * RPW < left) store8(dst, y);
       dst += RPW * sh;
@@ -154,8 +153,7 @@ prep_bwd_kernel(const __grid_constant__ PrepArgs a, int wt) {
     if (!a.weight[part]) continue;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      f2_split(gw[part][i], red[(warp * RPW + grp) * D + e + 2 * i], red[(warp * RPW + grp) * D + e + 2 * i + 1]);
+    for (int i = 0; i < 8; ++i) red[(warp * RPW + grp) * D + e + i] = gw[part][i];
     __syncthreads();
     for (int c = tid; c < D; c += kRwThreads) {
       float v = 0.f;

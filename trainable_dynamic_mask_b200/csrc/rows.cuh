@@ -7,22 +7,22 @@
 // of squares takes log2(D / 8) shuffles, and the partner of a rotated channel is either in the same
 // lane (neighbouring pairs) or in the same register of another lane of the row (halves).
 // These kernels would be bound by the instructions they issue before they are by memory (a first form
-// issued 250 for two rows, where reading and writing them leaves time for 170), so channels are kept in
-// pairs (one instruction for two float32 operations), and what belongs to a token or to its queries, keys
-// or values is worked out once for all their heads.
+// issued 210 for the two rows of a warp at 128 channels, where reading and writing them leaves time for 170;
+// this one 122), so what belongs to a token or to its queries, keys or values is worked out once for all
+// their heads, and addresses once for a chunk of rows.
 #pragma once
 
-#include "tc_ops.cuh"
+#include "common.cuh"
 
 namespace dma {
 
 // ---------------------------------------------------------------- eight channels
 
-// Eight consecutive channels as stored, and as four pairs of floats.
+// Eight consecutive channels as stored, and as floats.
 template <typename T> struct Raw8;
 template <> struct Raw8<uint16_t> { uint4 a; };
 template <> struct Raw8<float> { float4 a, b; };
-struct Pair8 { uint64_t v[4]; };
+struct Chan8 { float v[8]; };
 
 DMA_DEVINL Raw8<uint16_t> load_raw8(const uint16_t* p) { return {*reinterpret_cast<const uint4*>(p)}; }
 DMA_DEVINL Raw8<float> load_raw8(const float* p) {
@@ -45,36 +45,19 @@ DMA_DEVINL void widen8(const Raw8<float>& r, float (&v)[8]) {
   v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w;
   v[4] = r.b.x; v[5] = r.b.y; v[6] = r.b.z; v[7] = r.b.w;
 }
-template <typename T> DMA_DEVINL Pair8 pairs8(const Raw8<T>& r) {
-  float f[8];
-  widen8(r, f);
-  Pair8 p;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) p.v[i] = f2(f[2 * i], f[2 * i + 1]);
+template <typename T> DMA_DEVINL Chan8 channels8(const Raw8<T>& r) {
+  Chan8 p;
+  widen8(r, p.v);
   return p;
 }
 // The one rounding of a result (bf16: to nearest even).
-DMA_DEVINL void store8(uint16_t* p, const Pair8& y) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float a, b;
-    f2_split(y.v[i], a, b);
-    w[i] = pack_bf16x2(a, b);
-  }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+DMA_DEVINL void store8(uint16_t* p, const Chan8& y) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(y.v[0], y.v[1]), pack_bf16x2(y.v[2], y.v[3]),
+                                            pack_bf16x2(y.v[4], y.v[5]), pack_bf16x2(y.v[6], y.v[7]));
 }
-DMA_DEVINL void store8(float* p, const Pair8& y) {
-  float f[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f2_split(y.v[i], f[2 * i], f[2 * i + 1]);
-  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-}
-DMA_DEVINL float pair_sum(uint64_t v) {
-  float a, b;
-  f2_split(v, a, b);
-  return a + b;
+DMA_DEVINL void store8(float* p, const Chan8& y) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(y.v[0], y.v[1], y.v[2], y.v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(y.v[4], y.v[5], y.v[6], y.v[7]);
 }
 
 // Sum over the L neighbouring lanes of a row.
@@ -84,11 +67,11 @@ template <int L> DMA_DEVINL float row_sum(float x) {
   return x;
 }
 // Sum over a row of the products of two rows' channels.
-template <int L> DMA_DEVINL float row_dot(const Pair8& a, const Pair8& b) {
-  uint64_t s = f2_mul(a.v[0], b.v[0]);
+template <int L> DMA_DEVINL float row_dot(const Chan8& a, const Chan8& b) {
+  float s = a.v[0] * b.v[0];
 #pragma unroll
-  for (int i = 1; i < 4; ++i) s = f2_fma(a.v[i], b.v[i], s);
-  return row_sum<L>(pair_sum(s));
+  for (int i = 1; i < 8; ++i) s = fmaf(a.v[i], b.v[i], s);
+  return row_sum<L>(s);
 }
 
 // ---------------------------------------------------------------- rotation
@@ -119,7 +102,7 @@ DMA_DEVINL float2 turn_at(uint64_t rate, int position) {
 // same row, in lane `partner`, or swapped within a pair).  rot is a multiple of 16, so a lane's channels
 // are all rotated or none, and (halves) all in the first or all in the second half.
 struct LaneTurn {
-  Pair8 c, s;
+  Chan8 c, s;
   int partner;
   bool on;
 };
@@ -144,44 +127,34 @@ template <bool inter> DMA_DEVINL void lane_turn(LaneTurn& t, const float2* tab, 
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float4 v = q[i];
-      t.c.v[2 * i] = f2(v.x, v.x);
-      t.c.v[2 * i + 1] = f2(v.z, v.z);
-      t.s.v[2 * i] = f2(-plus * v.y, plus * v.y);
-      t.s.v[2 * i + 1] = f2(-plus * v.w, plus * v.w);
+      t.c.v[4 * i] = t.c.v[4 * i + 1] = v.x;
+      t.c.v[4 * i + 2] = t.c.v[4 * i + 3] = v.z;
+      t.s.v[4 * i] = -plus * v.y;
+      t.s.v[4 * i + 1] = plus * v.y;
+      t.s.v[4 * i + 2] = -plus * v.w;
+      t.s.v[4 * i + 3] = plus * v.w;
     }
   } else {
     const float sign = upper != back ? 1.f : -1.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float4 v = q[i];
-      t.c.v[i] = f2(v.x, v.z);
-      t.s.v[i] = f2(sign * v.y, sign * v.w);
+      t.c.v[2 * i] = v.x;
+      t.c.v[2 * i + 1] = v.z;
+      t.s.v[2 * i] = sign * v.y;
+      t.s.v[2 * i + 1] = sign * v.w;
     }
   }
 }
 
 // Channels beyond rot stay as they are, bit for bit.
-template <bool inter> DMA_DEVINL Pair8 rotate8(const Pair8& x, const LaneTurn& t) {
-  Pair8 y, o;
-  if (inter) {
+template <bool inter> DMA_DEVINL Chan8 rotate8(const Chan8& x, const LaneTurn& t) {
+  Chan8 y;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float a, b;
-      f2_split(x.v[i], a, b);
-      o.v[i] = f2(b, a);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float a, b;
-      f2_split(x.v[i], a, b);
-      o.v[i] = f2(__shfl_sync(0xffffffffu, a, t.partner), __shfl_sync(0xffffffffu, b, t.partner));
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 8; ++i) {
+    const float o = inter ? x.v[i ^ 1] : __shfl_sync(0xffffffffu, x.v[i], t.partner);
     y.v[i] = x.v[i];
-    if (t.on) y.v[i] = f2_fma(o.v[i], t.s.v[i], f2_mul(x.v[i], t.c.v[i]));
+    if (t.on) y.v[i] = fmaf(o, t.s.v[i], x.v[i] * t.c.v[i]);
   }
   return y;
 }
@@ -277,12 +250,12 @@ template <int NP, int U, int DEPTH> struct RowRing {
   }
 };
 
-// Blocks of a walk, and the warps that share a token: as many as it takes to give every SM a block, 8 at
-// most.
+// Blocks of a walk, and the warps that share a token: as many as it takes to give every warp of a full GPU
+// two shares (so that the last round weighs little), 8 at most.
 inline int walk_blocks(long long tokens, int per_sm, int* wt) {
   const int sms = sm_count();
   *wt = 1;
-  while (*wt < kRwWarps && tokens * *wt < (long long)sms * kRwWarps) *wt *= 2;
+  while (*wt < kRwWarps && tokens * *wt < 2LL * per_sm * sms * kRwWarps) *wt *= 2;
   const long long tpb = kRwWarps / *wt, need = (tokens + tpb - 1) / tpb;
   return (int)(need < (long long)per_sm * sms ? need : (long long)per_sm * sms);
 }
@@ -298,7 +271,7 @@ template <typename T> constexpr int fwd_rows() { return sizeof(T) == 2 ? 4 : 2; 
 template <typename T> using FwdRing = RowRing<sizeof(T) / 2, fwd_rows<T>(), 4>;
 
 // Queries and keys normed and rotated, values copied, from the projections (a.in, a.stride) to where Dest
-// says: dest.enter(tok, b, n, token) (every lane of the warp) is false if nothing of the token is written,
+// says: dest.enter(at, token) (every lane of the warp) is false if nothing of the token is written,
 // else token.position is its position and dest.row(part, token) the address of its first head's row, heads
 // dest.step(part) elements apart.
 template <typename T, int D, bool INTER, typename Dest>
@@ -333,7 +306,7 @@ row_walk_kernel(const __grid_constant__ PrepArgs a, const __grid_constant__ Dest
   auto work = [&](const Walk& at, const unsigned char* place) {
     if (have != at.tok) {
       have = at.tok;
-      live = dest.enter(at.tok, at.b, at.n, token);
+      live = dest.enter(at, token);
       if (live) {
         token_table(rate, a.rot >> 1, token.position, tab[warp]);
         lane_turn<INTER>(turn, tab[warp], start, upper, false);
@@ -352,18 +325,17 @@ row_walk_kernel(const __grid_constant__ PrepArgs a, const __grid_constant__ Dest
       return;
     }
     const T* wp = (const T*)a.weight[part];
-    Pair8 g;
-    if (wp != nullptr) g = pairs8(load_raw8(wp + e));
+    Chan8 g;
+    if (wp != nullptr) g = channels8(load_raw8(wp + e));
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      Pair8 x = pairs8(Ring::template read<T>(place + u * Ring::kRow, 0));
+      Chan8 x = channels8(Ring::template read<T>(place + u * Ring::kRow, 0));
       if (wp != nullptr) {
         const float r = rsqrtf(row_dot<L>(x, x) * (1.f / D) + a.eps);
-        const uint64_t rr = f2(r, r);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x.v[i] = f2_mul(f2_mul(x.v[i], rr), g.v[i]);
+        for (int i = 0; i < 8; ++i) x.v[i] *= r * g.v[i];
       }
-      const Pair8 y = rotate8<INTER>(x, turn);
+      const Chan8 y = rotate8<INTER>(x, turn);
       if (u * RPW < left) store8(dst, y);
       dst += RPW * sh;
     }
