@@ -19,15 +19,12 @@
 namespace dma {
 namespace {
 
-constexpr int kPlThreads = 128;
-constexpr int kPlWarps = kPlThreads / 32;
-
 DMA_DEVINL float exp_diff(float x, float m) { return fast_exp2((x - m) * kLog2e); }
 
 // Joins n partial results (m, l, o[D]) and writes the row's output.
-template <typename T, int D>
+template <typename T, int D, int NT>
 DMA_DEVINL void join_row(const float* part, int n, T* O, float* LSE) {
-  for (int c = threadIdx.x; c < D; c += kPlThreads) {
+  for (int c = threadIdx.x; c < D; c += NT) {
     float m = -INFINITY;
     for (int i = 0; i < n; ++i) m = fmaxf(m, __ldcg(part + (size_t)i * (D + 2)));
     const float ref = m == -INFINITY ? 0.f : m;
@@ -47,18 +44,20 @@ constexpr int kPlStages = 3;
 
 template <typename T> constexpr int list_keys() { return sizeof(T) == 2 ? 4 : 2; }   // keys of a group and stage
 // bytes of the ring: stages x keys x (K, V) x eight channels of every thread
-template <typename T> constexpr int list_smem() { return kPlStages * list_keys<T>() * 2 * 8 * sizeof(T) * kPlThreads; }
+template <typename T, int NT> constexpr int list_smem() { return kPlStages * list_keys<T>() * 2 * 8 * sizeof(T) * NT; }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kPlThreads, 4)
+// NT threads: 128, or one warp where the lists are short (behind a shared prefix), many of which then share
+// an SM.
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(NT, 512 / NT)
 paged_list_kernel(const T* __restrict__ Q, const T* __restrict__ K, const T* __restrict__ V,
                   const int4* __restrict__ rows, const int2* __restrict__ ent, float* __restrict__ part,
                   int32_t* __restrict__ counters, T* __restrict__ O, float* __restrict__ LSE, int H, int Hkv,
                   int page_shift, int sel_len, int n_split, int n_psplit, float scale) {
-  constexpr int L = D / 8, RPW = 32 / L, NG = kPlWarps * RPW;   // lanes of a row; groups of a warp, of the CTA
+  constexpr int L = D / 8, RPW = 32 / L, NG = (NT / 32) * RPW;   // lanes of a row; groups of a warp, of the CTA
   constexpr int U = list_keys<T>(), NP = sizeof(T) / 2;         // 16-byte pieces of a lane's eight channels
-  static_assert(kPagedSplit / NG <= 2 * L, "two entries a lane hold a group's keys");
-  static_assert(list_smem<T>() >= NG * D * 4, "the ring's place takes the groups' results at the end");
+  constexpr int E = kPagedSplit / NG / L;                       // entries of a lane
+  static_assert(list_smem<T, NT>() >= NG * D * 4, "the ring's place takes the groups' results at the end");
   extern __shared__ __align__(128) unsigned char ring[];
   float* so = reinterpret_cast<float*>(ring);   // [NG][D], when the ring is done with
   __shared__ float sm[NG], sl[NG];
@@ -68,27 +67,36 @@ paged_list_kernel(const T* __restrict__ Q, const T* __restrict__ K, const T* __r
   const int count = min(rows[row].x, sel_len);
   const int k0 = blockIdx.x * kPagedSplit, nk = min(count - k0, kPagedSplit);
   if (nk <= 0 && blockIdx.x > 0) return;   // the first CTA of a row works even if there is nothing
-  // the group's keys: k0 + j NG + grp; lane i of it holds the entries of j = i and i + L
+  // the group's keys: k0 + j NG + grp; lane i of it holds the entries of j = i, i + L, ..
   const int2* list = ent + (size_t)row * sel_len + k0;
-  int2 en[2] = {make_int2(0, 0), make_int2(0, 0)};
+  int2 en[E];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < E; ++i) {
     const int k = (lane % L + i * L) * NG + grp;
+    en[i] = make_int2(0, 0);
     if (k < nk) en[i] = list[k];
   }
+  // the entry of the group's key j
+  auto entry = [&](int j) {
+    int2 v = en[0];
+#pragma unroll
+    for (int i = 1; i < E; ++i)
+      if (j / L == i) v = en[i];
+    return make_int2(__shfl_sync(0xffffffffu, v.x, j % L, L), __shfl_sync(0xffffffffu, v.y, j % L, L));
+  };
   const int mask = (1 << page_shift) - 1;
   const uint32_t mine = smem_u32(ring) + tid * 16;
   auto issue = [&](int st) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int j = st * U + u, n = j * NG + grp < nk ? 16 : 0;
-      const int slot = __shfl_sync(0xffffffffu, j < L ? en[0].x : en[1].x, j % L, L);
+      const int slot = entry(j).x;
       const size_t at = (((((size_t)(slot >> page_shift) * Hkv + g) << page_shift) + (slot & mask)) * D) + e;
-      const uint32_t to = mine + (((st % kPlStages) * U + u) * 2 * NP) * kPlThreads * 16;
+      const uint32_t to = mine + (((st % kPlStages) * U + u) * 2 * NP) * NT * 16;
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        cp_async_16(to + i * kPlThreads * 16, K + at + i * 4, n);
-        cp_async_16(to + (NP + i) * kPlThreads * 16, V + at + i * 4, n);
+        cp_async_16(to + i * NT * 16, K + at + i * 4, n);
+        cp_async_16(to + (NP + i) * NT * 16, V + at + i * 4, n);
       }
     }
   };
@@ -109,7 +117,7 @@ paged_list_kernel(const T* __restrict__ Q, const T* __restrict__ K, const T* __r
     if (st + kPlStages - 1 < ns) issue(st + kPlStages - 1);
     cp_async_commit();
     cp_async_wait<kPlStages - 1>();
-    const unsigned char* from = ring + tid * 16 + ((st % kPlStages) * U * 2 * NP) * kPlThreads * 16;
+    const unsigned char* from = ring + tid * 16 + ((st % kPlStages) * U * 2 * NP) * NT * 16;
     float x[U], mx = m;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -117,14 +125,14 @@ paged_list_kernel(const T* __restrict__ Q, const T* __restrict__ K, const T* __r
 #pragma unroll
       for (int i = 0; i < NP; ++i)
         reinterpret_cast<uint4*>(&raw)[i] =
-            *reinterpret_cast<const uint4*>(from + (u * 2 * NP + i) * kPlThreads * 16);
+            *reinterpret_cast<const uint4*>(from + (u * 2 * NP + i) * NT * 16);
       float k[8], s = 0.f;
       widen8(raw, k);
 #pragma unroll
       for (int i = 0; i < 8; ++i) s = fmaf(k[i], q[i], s);
       s = row_sum<L>(s);
       const int j = st * U + u;
-      const float dl = __int_as_float(__shfl_sync(0xffffffffu, j < L ? en[0].y : en[1].y, j % L, L));
+      const float dl = __int_as_float(entry(j).y);
       x[u] = j * NG + grp < nk ? s + dl : -INFINITY;
       mx = fmaxf(mx, x[u]);
     }
@@ -140,7 +148,7 @@ paged_list_kernel(const T* __restrict__ Q, const T* __restrict__ K, const T* __r
 #pragma unroll
       for (int i = 0; i < NP; ++i)
         reinterpret_cast<uint4*>(&raw)[i] =
-            *reinterpret_cast<const uint4*>(from + (u * 2 * NP + NP + i) * kPlThreads * 16);
+            *reinterpret_cast<const uint4*>(from + (u * 2 * NP + NP + i) * NT * 16);
       const float p = exp_diff(x[u], ref);
       float v[8];
       widen8(raw, v);
@@ -171,7 +179,7 @@ paged_list_kernel(const T* __restrict__ Q, const T* __restrict__ K, const T* __r
       w[i] = exp_diff(sm[i], ref);
       lsum = fmaf(sl[i], w[i], lsum);
     }
-    for (int c = tid; c < D; c += kPlThreads) {
+    for (int c = tid; c < D; c += NT) {
       float o = 0.f;
 #pragma unroll
       for (int i = 0; i < NG; ++i) o = fmaf(so[i * D + c], w[i], o);
@@ -197,40 +205,43 @@ paged_list_kernel(const T* __restrict__ Q, const T* __restrict__ K, const T* __r
   __syncthreads();
   if (!last) return;
   __threadfence();
-  join_row<T, D>(prow, n_psplit + n_act, O + (size_t)row * D, LSE + row);
+  join_row<T, D, NT>(prow, n_psplit + n_act, O + (size_t)row * D, LSE + row);
 }
 
 // ---------------------------------------------------------------- shared prefix
 
-constexpr int kPcThreads = 128;
 constexpr int kPcTile = 64;    // candidates of a pipeline stage
 constexpr int kPcMost = 256;   // candidates of a CTA at most
 
 template <int D> constexpr int cand_smem() { return (64 + 4 * kPcTile) * D * 2; }   // Q, 2 x (K, V)
 
-// CTA = (part of a head's candidates, head, 16 R sequences).  Four warps: R groups of 16 sequences times
-// 4 / R groups of keys, so that a small batch still uses them all.  Tiles of 64 candidates' K and V rows
+// CTA = (part of a head's candidates, head, 16 R sequences).  Its warps (eight, four for R = 1) are R groups
+// of 16 sequences times 2 or 4 groups of keys: with four warps of a group to a tile, a warp's products and
+// exponentials are what a tile takes.  Tiles of 64 candidates' K and V rows
 // are gathered with 16-byte asynchronous copies (swizzled by row, conflict-free for ldmatrix), one tile
 // ahead.  A weight is split into two bf16 parts, both multiplied with V: one part alone would round every
 // weight to 8 bits, as much as the output's own rounding.
 // A candidate that a sequence did not select has weight exactly 0 there; if its V row holds an infinity or
 // NaN, 0 times that would still spoil the sum, so a tile with such a value is added up in plain
 // arithmetic that leaves weights of 0 out.
+template <int R> constexpr int cand_threads() { return R == 1 ? 128 : 256; }
+
 template <int D, int R>
-__global__ void __launch_bounds__(kPcThreads)
+__global__ void __launch_bounds__(cand_threads<R>(), 2)
 paged_cand_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ K, const uint16_t* __restrict__ V,
                   const int4* __restrict__ rows, const int32_t* __restrict__ crow, const int2* __restrict__ cent,
                   float* __restrict__ part, int B, int H, int Hkv, int page_shift, int cand_len, int cand_split,
                   int n_part, float scale) {
-  constexpr int CH = D / 8, KG = 4 / R, NT = 8 / KG, NO = D / 8;   // NT, NO: 8-wide tiles of keys, channels
+  constexpr int kPcThreads = cand_threads<R>(), kPcWarps = kPcThreads / 32;
+  constexpr int CH = D / 8, KG = kPcWarps / R, NT = 8 / KG, NO = D / 8;   // NT, NO: 8-wide tiles of keys, channels
   extern __shared__ __align__(128) unsigned char csm[];
   uint16_t* Qs = reinterpret_cast<uint16_t*>(csm);   // [16 R][D]
   uint16_t* Ks = Qs + 64 * D;                        // [2][64][D]
   uint16_t* Vs = Ks + 2 * kPcTile * D;               // [2][64][D]
-  __shared__ uint32_t ckey[kPcMost];
-  __shared__ float cdel[kPcMost];
+  __shared__ __align__(8) uint32_t ckey[kPcMost];
+  __shared__ __align__(8) float cdel[kPcMost];
   __shared__ int cslot[kPcMost];
-  __shared__ float gm[4][16], gl[4][16];
+  __shared__ float gm[kPcWarps][16], gl[kPcWarps][16];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.y, g = h / (H / Hkv), s0 = blockIdx.z * 16 * R;
   const int rg = warp / KG, kg = warp % KG;
@@ -283,18 +294,11 @@ paged_cand_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ K
   for (int n = 0; n < NO; ++n)
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
-  uint32_t qf[D / 16][4];
   for (int t = 0; t < nt; ++t) {
     if (t + 1 < nt) load_tile(t + 1);
     cp_async_commit();
     cp_async_wait<1>();
     __syncthreads();
-    if (t == 0) {
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        ldmatrix_x4(smem_u32(Qs) + swz(rg * 16 + (lane & 15), 2 * k + (lane >> 4), CH), qf[k][0], qf[k][1], qf[k][2],
-                    qf[k][3]);
-    }
     const uint32_t kb = smem_u32(Ks + (t & 1) * kPcTile * D), vb = smem_u32(Vs + (t & 1) * kPcTile * D);
     // an exponent of all ones anywhere in the V tile
     uint32_t odd = 0u;
@@ -315,25 +319,32 @@ paged_cand_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ K
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[n][i] = 0.f;
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k)
+    for (int k = 0; k < D / 16; ++k) {
+      uint32_t qf[4];
+      ldmatrix_x4(smem_u32(Qs) + swz(rg * 16 + (lane & 15), 2 * k + (lane >> 4), CH), qf[0], qf[1], qf[2], qf[3]);
 #pragma unroll
       for (int n = 0; n < NT; n += 2) {
         uint32_t b0, b1, b2, b3;
         ldmatrix_x4(kb + swz(key0 + n * 8 + (lane & 7) + (lane >> 4) * 8, 2 * k + ((lane >> 3) & 1), CH), b0, b1, b2, b3);
-        mma_bf16_16816(x[n], qf[k], b0, b1);
-        mma_bf16_16816(x[n + 1], qf[k], b2, b3);
+        mma_bf16_16816(x[n], qf, b0, b1);
+        mma_bf16_16816(x[n + 1], qf, b2, b3);
       }
+    }
     float mx[2] = {m[0], m[1]};
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+      const int j = t * kPcTile + key0 + n * 8 + 2 * (lane & 3);
+      const uint2 key = *reinterpret_cast<const uint2*>(ckey + j);
+      const float2 dl = *reinterpret_cast<const float2*>(cdel + j);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int j = t * kPcTile + key0 + n * 8 + 2 * (lane & 3) + (i & 1), r = i >> 1;
-        const uint32_t key = ckey[j];
-        const bool take = key > edge[r] || (key == edge[r] && key != 0u && c0 + j < cut[r]);
-        x[n][i] = take ? fmaf(x[n][i], scale, cdel[j]) : -INFINITY;
+        const int r = i >> 1;
+        const uint32_t k = (i & 1) ? key.y : key.x;
+        const bool take = k > edge[r] || (k == edge[r] && k != 0u && c0 + j + (i & 1) < cut[r]);
+        x[n][i] = take ? fmaf(x[n][i], scale, (i & 1) ? dl.y : dl.x) : -INFINITY;
         mx[r] = fmaxf(mx[r], x[n][i]);
       }
+    }
     float ref[2], keep[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -405,7 +416,7 @@ paged_cand_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ K
   cp_async_wait<0>();
   __syncthreads();
   // the warps' results side by side in the tiles' place, the key groups of a sequence joined
-  float* os = reinterpret_cast<float*>(Ks);   // [4 warps][16][D]
+  float* os = reinterpret_cast<float*>(Ks);   // [warps][16][D]
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
@@ -450,7 +461,7 @@ template <int D, int R>
 cudaError_t launch_cand(const PagedPlan& P, const void* Q, void* ws, cudaStream_t s) {
   const cudaError_t e = ensure_smem_limit(paged_cand_kernel<D, R>, cand_smem<D>());
   if (e != cudaSuccess) return e;
-  paged_cand_kernel<D, R><<<dim3(P.n_psplit, P.H, (P.B + 16 * R - 1) / (16 * R)), kPcThreads, cand_smem<D>(), s>>>(
+  paged_cand_kernel<D, R><<<dim3(P.n_psplit, P.H, (P.B + 16 * R - 1) / (16 * R)), cand_threads<R>(), cand_smem<D>(), s>>>(
       (const uint16_t*)Q, (const uint16_t*)P.K, (const uint16_t*)P.V, ws_ptr<int4>(ws, P.off_rows),
       ws_ptr<int32_t>(ws, P.off_crow), ws_ptr<int2>(ws, P.off_cent), ws_ptr<float>(ws, P.off_part), P.B, P.H, P.Hkv,
       P.page_shift, P.cand_len, P.cand_split, P.n_psplit + P.n_split, P.scale);
@@ -464,15 +475,24 @@ cudaError_t launch_cand_rows(const PagedPlan& P, const void* Q, void* ws, cudaSt
   return launch_cand<D, 4>(P, Q, ws, s);
 }
 
-template <typename T, int D>
-cudaError_t launch_list(const PagedPlan& P, const void* Q, void* ws, void* O, float* LSE, cudaStream_t s) {
-  const cudaError_t e = ensure_smem_limit(paged_list_kernel<T, D>, list_smem<T>());
+template <typename T, int D, int NT>
+cudaError_t launch_list_t(const PagedPlan& P, const void* Q, void* ws, void* O, float* LSE, cudaStream_t s) {
+  const cudaError_t e = ensure_smem_limit(paged_list_kernel<T, D, NT>, list_smem<T, NT>());
   if (e != cudaSuccess) return e;
-  paged_list_kernel<T, D><<<dim3(P.n_split, P.B * P.H), kPlThreads, list_smem<T>(), s>>>(
+  paged_list_kernel<T, D, NT><<<dim3(P.n_split, P.B * P.H), NT, list_smem<T, NT>(), s>>>(
       (const T*)Q, (const T*)P.K, (const T*)P.V, ws_ptr<int4>(ws, P.off_rows), ws_ptr<int2>(ws, P.off_ent),
       ws_ptr<float>(ws, P.off_part), ws_ptr<int32_t>(ws, P.off_count), (T*)O, LSE, P.H, P.Hkv, P.page_shift, P.sel_len,
       P.n_split, P.n_psplit, P.scale);
   return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_list(const PagedPlan& P, const void* Q, void* ws, void* O, float* LSE, cudaStream_t s) {
+  // behind a shared prefix a row lists about w (N - prefix) / N keys; one warp is enough for few of them, if
+  // there are rows enough to fill the GPU with such CTAs
+  if (P.shared && P.B * P.H >= 8 * sm_count() && (int64_t)P.w * (P.N - P.prefix) <= (int64_t)64 * P.N)
+    return launch_list_t<T, D, 32>(P, Q, ws, O, LSE, s);
+  return launch_list_t<T, D, 128>(P, Q, ws, O, LSE, s);
 }
 
 }  // namespace

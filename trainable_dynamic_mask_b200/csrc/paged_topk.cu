@@ -57,13 +57,14 @@ template <int NW> DMA_DEVINL int2 warps_before(int x, int* buf) {
   return make_int2(__shfl_sync(0xffffffffu, v - own, warp), __shfl_sync(0xffffffffu, v, NW - 1));
 }
 
-template <SelMode M, int NT, bool SIEVE>
-__global__ void __launch_bounds__(NT, NT == 512 ? 2 : 6)
+// CL: clusters of more than one CTA.
+template <SelMode M, int NT, bool SIEVE, bool CL>
+__global__ void __launch_bounds__(NT, NT == 512 ? 2 : NT == 256 ? 4 : 8)
 paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict__ sel, int2* __restrict__ ent,
                     int32_t* __restrict__ crow, int32_t* __restrict__ cand, int2* __restrict__ cent,
                     int32_t* __restrict__ counters, int32_t* __restrict__ status, int cap, int page_cap,
                     int list_cap) {
-  constexpr int NW = NT / 32, BINS = 4 * NT, LB = NT == 512 ? 11 : 9;
+  constexpr int NW = NT / 32, BINS = 4 * NT, LB = NT == 512 ? 11 : NT == 256 ? 10 : 9;
   static_assert(BINS == 1 << LB, "four counters a thread");
   static_assert(!SIEVE || M == kRows, "candidates and their rest are short or few");
   extern __shared__ __align__(16) uint32_t keys[];   // [cap] this CTA's stretch, as far as it fits
@@ -79,11 +80,14 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
   __shared__ int found_bin, found_above, found_count;
   __shared__ uint32_t found_key;
   cg::cluster_group cl = cg::this_cluster();
-  const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  constexpr int kMost = CL ? kPsMaxCluster : 1;
+  const int C = CL ? (int)cl.num_blocks() : 1, rank = CL ? (int)cl.block_rank() : 0;
   auto all_sync = [&]() {
-    if (C > 1) cl.sync();
+    if (CL) cl.sync();
     else __syncthreads();
   };
+  // p in the shared memory of CTA r of the cluster
+  auto of = [&](auto* p, int r) { return CL ? cl.map_shared_rank(p, r) : p; };
   const int row = blockIdx.y, h = M == kCandidates ? row : row % P.H, b = M == kCandidates ? 0 : row / P.H;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int W = row_window(P.w_heads, h, P.H, P.w);
@@ -102,7 +106,7 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
   const bool idle = len <= 0 || bad;
   const int n1p = (n1 + 3) & ~3;
   const int n = idle ? 0 : n1p + (len - base);
-  const int seg = ((n + C - 1) / C + 3) & ~3;
+  const int seg = CL ? ((n + C - 1) / C + 3) & ~3 : n;
   const int i0 = min(rank * seg, n), i1 = min(i0 + seg, n), ns = i1 - i0;
   const int2* ce = M == kRest ? cent + (size_t)h * P.cand_len : nullptr;
   // what the steps after the first reading work on: the stretch (the first `res` keys resident, what lies
@@ -117,7 +121,7 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
       bad = true;
       pg = 0;
     }
-    pages[i] = pg * P.H + h;
+    pages[i] = pg;
   }
   if (tid == 0) {
     sh.kmin = 0xffffffffu;
@@ -131,8 +135,7 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
   *reinterpret_cast<int4*>(hist + 4 * tid) = make_int4(0, 0, 0, 0);
   if (SIEVE) *reinterpret_cast<int4*>(mhist + 4 * tid) = make_int4(0, 0, 0, 0);
   __syncthreads();
-  // row of the delta pages (page number x H + h) that holds a position
-  auto page_row = [&](int pos) -> int {
+  auto page_of = [&](int pos) -> int {
     const int i = (pos >> P.page_shift) - tab0;
     if (i < page_cap) return pages[i];
     int pg = __ldg(tab + tab0 + i);
@@ -140,11 +143,14 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
       bad = true;
       pg = 0;
     }
-    return pg * P.H + h;
+    return pg;
   };
-  auto slot_of = [&](int pos) -> int { return (page_row(pos) / P.H << P.page_shift) + (pos & (page - 1)); };
+  auto slot_of = [&](int pos) -> int { return (page_of(pos) << P.page_shift) + (pos & (page - 1)); };
+  // values of this head, of page pg
+  const float* head = P.delta + ((size_t)h << P.page_shift);
+  auto values_of = [&](int pg) { return head + ((size_t)(unsigned)(pg * P.H) << P.page_shift); };   // n_pages H < 2^31
   auto value4 = [&](int pos) -> float4 {
-    return *reinterpret_cast<const float4*>(P.delta + ((size_t)page_row(pos) << P.page_shift) + (pos & (page - 1)));
+    return *reinterpret_cast<const float4*>(values_of(page_of(pos)) + (pos & (page - 1)));
   };
   // order keys of indices i .. i + 3 (i a multiple of 4); 0 where there is nothing
   auto load4 = [&](int i) -> uint4 {
@@ -188,12 +194,12 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
     const int b4 = (NT - 1 - tid) * 4;
     int4 c = make_int4(0, 0, 0, 0);
     {
-      int4 o[kPsMaxCluster];
+      int4 o[kMost];
 #pragma unroll
-      for (int r = 0; r < kPsMaxCluster; ++r)
-        o[r] = r < C ? *reinterpret_cast<const int4*>(cl.map_shared_rank(counts + b4, r)) : make_int4(0, 0, 0, 0);
+      for (int r = 0; r < kMost; ++r)
+        o[r] = r < C ? *reinterpret_cast<const int4*>(of(counts + b4, r)) : make_int4(0, 0, 0, 0);
 #pragma unroll
-      for (int r = 0; r < kPsMaxCluster; ++r) {
+      for (int r = 0; r < kMost; ++r) {
         c.x += o[r].x; c.y += o[r].y; c.z += o[r].z; c.w += o[r].w;
       }
     }
@@ -235,16 +241,16 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
       if (wbad) to.bad = 1;
     }
     all_sync();
-    PsShared o[kPsMaxCluster];
+    PsShared o[kMost];
 #pragma unroll
-    for (int r = 0; r < kPsMaxCluster; ++r)
+    for (int r = 0; r < kMost; ++r)
       if (r < C) {
-        const PsShared* q = cl.map_shared_rank(&to, r);
+        const PsShared* q = of(&to, r);
         o[r].kmin = q->kmin; o[r].kmax = q->kmax; o[r].valid = q->valid; o[r].bad = q->bad;
       }
     kmin = o[0].kmin; kmax = o[0].kmax; valid = o[0].valid; bad = o[0].bad != 0;
 #pragma unroll
-    for (int r = 1; r < kPsMaxCluster; ++r)
+    for (int r = 1; r < kMost; ++r)
       if (r < C) {
         kmin = min(kmin, o[r].kmin);
         kmax = max(kmax, o[r].kmax);
@@ -286,8 +292,7 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           const int pu = pos + u * 128;
-          f[u] = *reinterpret_cast<const float4*>(P.delta + (pu & (page - 1)) +
-                                                  ((size_t)pages[(pu >> P.page_shift) - tab0] << P.page_shift));
+          f[u] = *reinterpret_cast<const float4*>(values_of(pages[(pu >> P.page_shift) - tab0]) + (pu & (page - 1)));
         }
       } else {
 #pragma unroll
@@ -406,7 +411,7 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
       valid = tid == 0 ? items : 0;
       publish(sh, kmin, kmax, valid);
       sieved = true;
-      for (int r = 0; r < C; ++r) sieved = sieved && cl.map_shared_rank(&sh, r)->members == 0;
+      for (int r = 0; r < C; ++r) sieved = sieved && of(&sh, r)->members == 0;
     }
     if (!sieved) {
       all_sync();                          // all have seen it
@@ -477,8 +482,8 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
         all_sync();
         int m = 0;
         for (int r = 0; r < C; ++r) {
-          const int mr = cl.map_shared_rank(&sh, r)->members;
-          if (tid < mr) every[m + tid] = *cl.map_shared_rank(list + tid, r);
+          const int mr = of(&sh, r)->members;
+          if (tid < mr) every[m + tid] = *of(list + tid, r);
           m += mr;
         }
         __syncthreads();
@@ -570,15 +575,15 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
     tot[u] = v.y;
   }
   if (M != kRest) mine[0] = mine[1] = tot[0] = tot[1] = 0;
-  if (C > 1) {
+  if (CL) {
     if (tid == 0) sh.count = make_int4(tot[0], tot[1], tot[2], tot[3]);
     cl.sync();
-    int4 o[kPsMaxCluster];
+    int4 o[kMost];
 #pragma unroll
-    for (int r = 0; r < kPsMaxCluster; ++r)
-      o[r] = r < C ? cl.map_shared_rank(&sh, r)->count : make_int4(0, 0, 0, 0);
+    for (int r = 0; r < kMost; ++r)
+      o[r] = r < C ? of(&sh, r)->count : make_int4(0, 0, 0, 0);
 #pragma unroll
-    for (int r = 0; r < kPsMaxCluster; ++r) {
+    for (int r = 0; r < kMost; ++r) {
       const int oc[4] = {o[r].x, o[r].y, o[r].z, o[r].w};
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -683,18 +688,18 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
       }
     }
   }
-  if (C > 1) cl.sync();   // no CTA leaves while another may still read its shared memory
+  if (CL) cl.sync();   // no CTA leaves while another may still read its shared memory
 }
 
 // cap: words of shared memory for keys.
-template <SelMode M, int NT, bool SIEVE>
+template <SelMode M, int NT, bool SIEVE, bool CL>
 cudaError_t launch_select_t(const PagedPlan& P, int n_rows, int n, int C, int cap, int list_cap, void* ws,
                             cudaStream_t s) {
   const int seg = ((n + C - 1) / C + 3) & ~3;
   int page_cap = (seg >> P.page_shift) + 2;
   if (page_cap > 4096) page_cap = 4096;
   const size_t smem = (size_t)(cap + page_cap) * 4;
-  const cudaError_t e = ensure_smem_limit(paged_select_kernel<M, NT, SIEVE>, (int)smem);
+  const cudaError_t e = ensure_smem_limit(paged_select_kernel<M, NT, SIEVE, CL>, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(C, n_rows);
@@ -707,8 +712,8 @@ cudaError_t launch_select_t(const PagedPlan& P, int n_rows, int n, int C, int ca
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_select_kernel<M, NT, SIEVE>, P, ws_ptr<int32_t>(ws, P.off_rows),
+  cfg.numAttrs = CL ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, paged_select_kernel<M, NT, SIEVE, CL>, P, ws_ptr<int32_t>(ws, P.off_rows),
                             ws_ptr<int32_t>(ws, P.off_sel), ws_ptr<int2>(ws, P.off_ent),
                             ws_ptr<int32_t>(ws, P.off_crow), ws_ptr<int32_t>(ws, P.off_cand),
                             ws_ptr<int2>(ws, P.off_cent), ws_ptr<int32_t>(ws, P.off_count),
@@ -731,16 +736,22 @@ cudaError_t launch_select(const PagedPlan& P, int n_rows, int n, void* ws, cudaS
       list_cap = (list_cap + 7) & ~7;
       const int cap = 2 * list_cap + list_cap / 2;
       if (seg <= 65536 && list_cap <= 128 * kPsMaxBatches && cap <= 36864)
-        return launch_select_t<M, 512, true>(P, n_rows, n, C, cap, list_cap, ws, s);
+        return C > 1 ? launch_select_t<M, 512, true, true>(P, n_rows, n, C, cap, list_cap, ws, s)
+                     : launch_select_t<M, 512, true, false>(P, n_rows, n, C, cap, list_cap, ws, s);
     }
   }
-  // clusters: stretches of at most 16384 values, and for few rows as many CTAs as give every SM one, down to
-  // stretches of 2048; short rows in large numbers go to small CTAs, more of which share an SM
+  // clusters: stretches of at most 16384 values, and for few rows as many CTAs as there are SMs for (more
+  // would wait: a cluster needs its SMs side by side), down to stretches of 2048; short rows in large
+  // numbers go to small CTAs, more of which share an SM
   int C = 1;
-  while (C < kPsMaxCluster && ((n + C - 1) / C > 16384 || (n_rows * C < sms && (n + C - 1) / C > 2048))) C *= 2;
+  while (C < kPsMaxCluster && ((n + C - 1) / C > 16384 || (2 * n_rows * C <= sms && (n + C - 1) / C > 2048))) C *= 2;
   const int seg = ((n + C - 1) / C + 3) & ~3, cap = seg + 4 < 40960 ? seg + 4 : 40960;
-  if (seg <= 4096 && n_rows * C >= 4 * sms) return launch_select_t<M, 128, false>(P, n_rows, n, C, cap, 0, ws, s);
-  return launch_select_t<M, 512, false>(P, n_rows, n, C, cap, 0, ws, s);
+  if (C > 1) return launch_select_t<M, 512, false, true>(P, n_rows, n, C, cap, 0, ws, s);
+  if (n_rows >= 4 * sms) {
+    if (seg <= 4096) return launch_select_t<M, 128, false, false>(P, n_rows, n, C, cap, 0, ws, s);
+    if (seg <= 8192) return launch_select_t<M, 256, false, false>(P, n_rows, n, C, cap, 0, ws, s);
+  }
+  return launch_select_t<M, 512, false, false>(P, n_rows, n, C, cap, 0, ws, s);
 }
 
 }  // namespace
