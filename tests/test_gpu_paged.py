@@ -246,6 +246,9 @@ PREFIXED = {
     "heads": ([512, 700, 513], 512, 4, 2, 64, 16, "bf16", 200, dict(w_heads=[200, 1, 0, 999])),
     "batch": ([4096 + i for i in range(70)], 4096, 4, 2, 128, 64, "bf16", 600, {}),
     "long": ([40960, 50001], 40960, 2, 1, 128, 64, "bf16", 2048, {}),
+    "crossing": ([4096, 4700, 4200, 4097, 4150], 4096, 2, 1, 64, 64, "bf16", 512, {}),
+    "crossing_ties": ([1024 + 40 * i for i in range(12)], 1024, 2, 1, 64, 64, "bf16", 400, dict(delta="levels")),
+    "tiny_window": ([512, 600, 513, 530], 512, 2, 1, 64, 16, "bf16", 3, {}),
     "idle_first": ([0, 100, 96], 96, 2, 2, 64, 32, "bf16", 40, {}),
     "float": ([64, 100, 90], 64, 2, 1, 64, 16, "f32", 30, {}),
     "alone": ([90], 64, 2, 1, 64, 16, "bf16", 30, {}),
@@ -265,6 +268,18 @@ def test_shared_prefix(name):
     again = c.run(out[0])
     for x, y in zip(out, again):
         assert c.torch.equal(x, y)
+
+
+def test_shared_prefix_any_bits_and_many_that_pass():
+    """Selections alone: any float32 pattern, and own keys that push out more candidates than are kept in order."""
+    for kind, seed in (("bits", 41), ("bits", 42), ("gate", 43)):
+        c = Cache([2048, 2100, 2048 + 900, 2049, 0, 2700], 6, 6, 64, 32, "bf16", 300, seed=seed, prefix=2048, delta=kind)
+        if kind == "gate":
+            c.delta[c.table[2, 64:].long()] += 0.4
+            c.delta[c.table[5, 64:66].long()] += 0.4
+        c.dma.paged_topk(c.p, c.c, c.ws)
+        c.torch.cuda.synchronize()
+        c.check_selection()
 
 
 def test_shared_prefix_masked_places_may_hold_anything():

@@ -123,6 +123,7 @@ cudaError_t launch_prep_bwd(const PrepArgs& a, bool bf16, int d, float* dq_weigh
 // ---------------------------------------------------------------- paged cache (paged*.cu)
 constexpr int kPagedErr = 0x10000000;   // status bit: a page number or a length out of range
 constexpr int kPagedSplit = 256;        // selected keys per CTA of the attention over one row's list
+constexpr int kPagedTail = 64;          // last candidates of a shared prefix that are kept in order
 
 // Resolved paged problem: what the kernels read, and the workspace plan.
 struct PagedPlan {
@@ -145,8 +146,10 @@ struct PagedPlan {
   size_t off_ent;           // int2 [B*H, sel_len]: {slot of the cache, delta bits} beside off_sel
   size_t off_crow;          // int32 [H]: candidates of the head (-1: a bad page among the prefix's)
   size_t off_cent;          // int2 [H, cand_len]: as off_ent, beside off_cand
+  size_t off_tail;          // int2 [H, kPagedTail + 1]: {order key, number} of the head's last candidates, the
+                            // very last first; then {how many of them are known, 0}
   size_t off_count;         // int32 [B*H]: partial results written; 0 before and after every attention call
-  size_t off_part;          // f32 [B*H][n_psplit + n_split][d + 2]: m, l, o
+  size_t off_part;          // f32 [B*H][n_psplit + n_split][d + 4]: o, m, l, -, -
   size_t bytes;
 };
 struct PagedAppendArgs {

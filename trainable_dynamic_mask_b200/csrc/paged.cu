@@ -61,8 +61,9 @@ dma_status_t paged_plan(const dma_params_t* p, const dma_pages_t* c, PagedPlan* 
   P->off_ent = take(BH * P->sel_len * 8);
   P->off_crow = take((size_t)P->H * 4);
   P->off_cent = take((size_t)P->H * P->cand_len * 8);
+  P->off_tail = take((size_t)P->H * (kPagedTail + 1) * 8);
   P->off_count = take(BH * 4);
-  P->off_part = take(BH * (P->n_psplit + P->n_split) * (size_t)(P->d + 2) * 4);
+  P->off_part = take(BH * (P->n_psplit + P->n_split) * (size_t)(P->d + 4) * 4);
   P->bytes = off;
   return DMA_OK;
 }

@@ -21,23 +21,43 @@ namespace {
 
 DMA_DEVINL float exp_diff(float x, float m) { return fast_exp2((x - m) * kLog2e); }
 
-// Joins n partial results (m, l, o[D]) and writes the row's output.
-template <typename T, int D, int NT>
-DMA_DEVINL void join_row(const float* part, int n, T* O, float* LSE) {
-  for (int c = threadIdx.x; c < D; c += NT) {
-    float m = -INFINITY;
-    for (int i = 0; i < n; ++i) m = fmaxf(m, __ldcg(part + (size_t)i * (D + 2)));
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o = 0.f;
-    for (int i = 0; i < n; ++i) {
-      const float* p = part + (size_t)i * (D + 2);
-      const float w = exp_diff(__ldcg(p), ref);
-      l = fmaf(__ldcg(p + 1), w, l);
-      o = fmaf(__ldcg(p + 2 + c), w, o);
+// Writes the row's output from its sums: nothing kept: 0 and -inf; a NaN stays.
+template <typename T> DMA_DEVINL void put_channel(T* O, float o, float l) {
+  store_from_f32(O, l > 0.f ? o / l : (l == 0.f ? 0.f : l));
+}
+DMA_DEVINL void put_lse(float* LSE, float m, float l) {
+  *LSE = l > 0.f ? m + logf(l) : (l == 0.f ? -INFINITY : l);
+}
+
+// Joins n partial results (o[D], m, l) with a row's running o (this thread's V channels from c), m and l.
+template <int D, int V> DMA_DEVINL void join(const float* part, int n, int c, float& m, float& l, float (&o)[V]) {
+  float big = m;
+  for (int i = 0; i < n; ++i) big = fmaxf(big, __ldcg(part + (size_t)i * (D + 4) + D));
+  const float ref = big == -INFINITY ? 0.f : big;
+  const float w0 = exp_diff(m, ref);
+  l *= w0;
+#pragma unroll
+  for (int u = 0; u < V; ++u) o[u] *= w0;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float* p = part + (size_t)i * (D + 4);
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + D));
+    float v[V];
+    if constexpr (V == 4) {
+      const float4 q = __ldcg(reinterpret_cast<const float4*>(p + c));
+      v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+    } else if constexpr (V == 2) {
+      const float2 q = __ldcg(reinterpret_cast<const float2*>(p + c));
+      v[0] = q.x; v[1] = q.y;
+    } else {
+      v[0] = __ldcg(p + c);
     }
-    store_from_f32(O + c, l > 0.f ? o / l : (l == 0.f ? 0.f : l));   // nothing kept: 0; NaN stays
-    if (c == 0) *LSE = l > 0.f ? ref + logf(l) : (l == 0.f ? -INFINITY : l);
+    const float w = exp_diff(ml.x, ref);
+    l = fmaf(ml.y, w, l);
+#pragma unroll
+    for (int u = 0; u < V; ++u) o[u] = fmaf(v[u], w, o[u]);
   }
+  m = big;
 }
 
 constexpr int kPlStages = 3;
@@ -166,46 +186,57 @@ paged_list_kernel(const T* __restrict__ Q, const T* __restrict__ K, const T* __r
   }
   __syncthreads();
   const int n_act = count > 0 ? (count + kPagedSplit - 1) / kPagedSplit : 1;
-  float* prow = part + (size_t)row * (n_psplit + n_split) * (D + 2);
-  float* out = prow + (size_t)(n_psplit + blockIdx.x) * (D + 2);
-  {
-    float M = sm[0];
+  constexpr int VC = D / NT > 1 ? D / NT : 1;   // channels of a thread
+  const int c = tid * VC;
+  float M = sm[0];
 #pragma unroll
-    for (int i = 1; i < NG; ++i) M = fmaxf(M, sm[i]);
+  for (int i = 1; i < NG; ++i) M = fmaxf(M, sm[i]);
+  float lsum = 0.f, o[VC];
+  {
     const float ref = M == -INFINITY ? 0.f : M;
-    float w[NG], lsum = 0.f;
+#pragma unroll
+    for (int u = 0; u < VC; ++u) o[u] = 0.f;
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
-      w[i] = exp_diff(sm[i], ref);
-      lsum = fmaf(sl[i], w[i], lsum);
-    }
-    for (int c = tid; c < D; c += NT) {
-      float o = 0.f;
+      const float w = exp_diff(sm[i], ref);
+      lsum = fmaf(sl[i], w, lsum);
+      if (c < D)
 #pragma unroll
-      for (int i = 0; i < NG; ++i) o = fmaf(so[i * D + c], w[i], o);
-      if (n_act + n_psplit == 1) {
-        store_from_f32(O + (size_t)row * D + c, lsum > 0.f ? o / lsum : (lsum == 0.f ? 0.f : lsum));
-        if (c == 0) LSE[row] = lsum > 0.f ? ref + logf(lsum) : (lsum == 0.f ? -INFINITY : lsum);
-      } else {
-        out[2 + c] = o;
-        if (c == 0) {
-          out[0] = M;
-          out[1] = lsum;
-        }
-      }
+        for (int u = 0; u < VC; ++u) o[u] = fmaf(so[i * D + c + u], w, o[u]);
     }
   }
-  if (n_act + n_psplit == 1) return;
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) {
-    last = atomicAdd(counters + row, 1) == n_act - 1;
-    if (last) counters[row] = 0;   // as the next call expects it
+  float* prow = part + (size_t)row * (n_psplit + n_split) * (D + 4);
+  int others = n_psplit;   // partial results to join
+  if (n_act > 1) {
+    float* out = prow + (size_t)(n_psplit + blockIdx.x) * (D + 4);
+    if (c < D)
+#pragma unroll
+      for (int u = 0; u < VC; ++u) out[c + u] = o[u];
+    if (tid == 0) {
+      out[D] = M;
+      out[D + 1] = lsum;
+    }
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+      last = atomicAdd(counters + row, 1) == n_act - 1;
+      if (last) counters[row] = 0;   // as the next call expects it
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    // all of them in their order, this CTA's among them
+    others = n_psplit + n_act;
+    M = -INFINITY;
+    lsum = 0.f;
+#pragma unroll
+    for (int u = 0; u < VC; ++u) o[u] = 0.f;
   }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  join_row<T, D, NT>(prow, n_psplit + n_act, O + (size_t)row * D, LSE + row);
+  if (c >= D) return;
+  if (others > 0) join<D, VC>(prow, others, c, M, lsum, o);
+#pragma unroll
+  for (int u = 0; u < VC; ++u) put_channel(O + (size_t)row * D + c + u, o[u], lsum);
+  if (c == 0) put_lse(LSE + row, M == -INFINITY ? 0.f : M, lsum);
 }
 
 // ---------------------------------------------------------------- shared prefix
@@ -448,12 +479,9 @@ paged_cand_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ K
       sum = fmaf(gl[w0 + q][i], w, sum);
       a.x = fmaf(v.x, w, a.x); a.y = fmaf(v.y, w, a.y); a.z = fmaf(v.z, w, a.z); a.w = fmaf(v.w, w, a.w);
     }
-    float* out = part + (((size_t)(s0 + r) * H + h) * n_part + blockIdx.x) * (D + 2);
-    if (c == 0) {
-      out[0] = M;
-      out[1] = sum;
-    }
-    out[2 + c] = a.x; out[3 + c] = a.y; out[4 + c] = a.z; out[5 + c] = a.w;
+    float* out = part + (((size_t)(s0 + r) * H + h) * n_part + blockIdx.x) * (D + 4);
+    if (c == 0) *reinterpret_cast<float2*>(out + D) = make_float2(M, sum);
+    *reinterpret_cast<float4*>(out + c) = a;
   }
 }
 

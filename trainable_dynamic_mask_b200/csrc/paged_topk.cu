@@ -18,7 +18,9 @@
 //
 // With a shared prefix the same kernel first selects the prefix's best w for each head (the candidates),
 // then takes each row's best w of (candidates, the row's own positions behind the prefix): the best of a
-// union are among the best of its parts, and delta does not depend on the query.
+// union are among the best of its parts, and delta does not depend on the query.  Few of a row's own keys
+// pass the last candidate, as a rule; they compete with as many of the last candidates, which are kept in
+// order for that (rest_by_tail), and only where they are more is the row counted like any other.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -57,12 +59,96 @@ template <int NW> DMA_DEVINL int2 warps_before(int x, int* buf) {
   return make_int2(__shfl_sync(0xffffffffu, v - own, warp), __shfl_sync(0xffffffffu, v, NW - 1));
 }
 
+// A row's selection where all w candidates would fill it and at most kPagedTail - 1 of its own keys pass the
+// last of them: each of those m keys and of the last m candidates is in unless m of these 2 m come after it.
+// keys, where: room for kPagedTail; false (for the whole block): not that simple, nothing written.
+template <int NT>
+DMA_DEVINL bool rest_by_tail(const PagedPlan& P, const int32_t* tab, int h, int len, int W, int n1, const int2* tail,
+                             uint32_t* keys, int* where, int* buf, int4* rec, int32_t* lp, int2* le, bool& bad) {
+  const int tid = threadIdx.x, lane = tid & 31, page = 1 << P.page_shift;
+  const int known = tail[kPagedTail].x;
+  if (n1 < W || known <= 0) return false;
+  const uint32_t last = (uint32_t)tail[0].x;
+  const float* head = P.delta + ((size_t)h << P.page_shift);
+  int m = 0;   // keys that pass so far
+  for (int p0 = P.prefix; p0 < len; p0 += NT * 4) {
+    const int pos = p0 + tid * 4;
+    uint32_t k[4] = {0u, 0u, 0u, 0u};
+    bool wrong = false;
+    if (pos < len) {
+      const int pg = __ldg(tab + (pos >> P.page_shift));
+      wrong = pg < 0 || pg >= P.n_pages;
+      if (!wrong) {
+        const float4 f = *reinterpret_cast<const float4*>(head + ((size_t)(unsigned)(pg * P.H) << P.page_shift) +
+                                                          (pos & (page - 1)));
+        k[0] = order_key(f.x);
+        if (pos + 1 < len) k[1] = order_key(f.y);
+        if (pos + 2 < len) k[2] = order_key(f.z);
+        if (pos + 3 < len) k[3] = order_key(f.w);
+      }
+    }
+    unsigned own = 0u;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) own |= k[u] > last ? 1u << u : 0u;   // a tie goes to the candidate
+    int incl = __popc(own);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const int2 w = warps_before<NT / 32>(__shfl_sync(0xffffffffu, incl, 31), buf);
+    int at = m + w.x + incl - __popc(own);
+    m += w.y;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (own >> u & 1u) {
+        if (at < kPagedTail) {
+          keys[at] = k[u];
+          where[at] = pos + u;
+        }
+        ++at;
+      }
+    if (__syncthreads_or(wrong)) {
+      bad = true;
+      return false;
+    }
+    if (m >= known) return false;
+  }
+  // survivors: threads 0 .. m - 1; the last m candidates: threads 64 .. 64 + m - 1
+  int after = 0;
+  if (tid < m) {
+    const uint32_t k = keys[tid];
+    for (int i = 0; i < m; ++i) {
+      after += keys[i] < k || (keys[i] == k && i > tid);
+      after += (uint32_t)tail[i].x < k;
+    }
+  } else if (tid >= 64 && tid < 64 + m) {
+    const uint32_t k = (uint32_t)tail[tid - 64].x;
+    after = tid - 64;
+    for (int i = 0; i < m; ++i) after += keys[i] <= k;
+  }
+  const bool in = after >= m;
+  const int out_c = __syncthreads_count(tid >= 64 && tid < 64 + m && !in);   // candidates that give way
+  const unsigned mine = __ballot_sync(0xffffffffu, tid < m && in);
+  if (lane == 0 && tid < 64) buf[tid >> 5] = __popc(mine);
+  __syncthreads();
+  if (tid < m && in) {
+    const int at = (tid >= 32 ? buf[0] : 0) + __popc(mine & ((1u << lane) - 1u));
+    const int pos = where[tid], pg = __ldg(tab + (pos >> P.page_shift));
+    const uint32_t k = keys[tid];
+    lp[at] = pos;
+    le[at] = make_int2((pg << P.page_shift) + (pos & (page - 1)), (int)((k & 0x80000000u) ? k ^ 0x80000000u : ~k));
+  }
+  if (tid == 0) *rec = make_int4(out_c, tail[out_c].x, tail[out_c].y + 1, W - out_c);
+  return true;
+}
+
 // CL: clusters of more than one CTA.
 template <SelMode M, int NT, bool SIEVE, bool CL>
 __global__ void __launch_bounds__(NT, NT == 512 ? 2 : NT == 256 ? 4 : 8)
 paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict__ sel, int2* __restrict__ ent,
                     int32_t* __restrict__ crow, int32_t* __restrict__ cand, int2* __restrict__ cent,
-                    int32_t* __restrict__ counters, int32_t* __restrict__ status, int cap, int page_cap,
+                    int2* __restrict__ tail, int32_t* __restrict__ counters, int32_t* __restrict__ status, int cap, int page_cap,
                     int list_cap) {
   constexpr int NW = NT / 32, BINS = 4 * NT, LB = NT == 512 ? 11 : NT == 256 ? 10 : 9;
   static_assert(BINS == 1 << LB, "four counters a thread");
@@ -104,6 +190,15 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
   }
   if (len > P.N || (len > 0 && len < (M == kCandidates ? 0 : P.prefix))) bad = true;
   const bool idle = len <= 0 || bad;
+  if constexpr (M == kRest && !CL) {
+    if (!idle && rest_by_tail<NT>(P, tab, h, len, W, n1, tail + (size_t)h * (kPagedTail + 1), list,
+                                  reinterpret_cast<int*>(every), wbuf[0], reinterpret_cast<int4*>(rows) + row,
+                                  sel + (size_t)row * P.sel_len, ent + (size_t)row * P.sel_len, bad)) {
+      if (tid == 0) counters[row] = 0;
+      return;
+    }
+    __syncthreads();
+  }
   const int n1p = (n1 + 3) & ~3;
   const int n = idle ? 0 : n1p + (len - base);
   const int seg = CL ? ((n + C - 1) / C + 3) & ~3 : n;
@@ -187,9 +282,9 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
     }
   };
 
-  // the counter (of 4 NT, summed over the cluster) that holds the want-th largest key, `above` keys lying
+  // the counter (of 4 NT, summed over the cluster if whole) that holds the want-th largest key, `above` keys lying
   // above all of them: found_bin, found_above, found_count
-  auto find_bin = [&](int* counts, int above, int want, int* buf) {
+  auto find_bin = [&](int* counts, int above, int want, int* buf, bool whole = true) {
     // thread t sums counters 4 t' .. 4 t' + 3, t' = NT - 1 - t: from the top
     const int b4 = (NT - 1 - tid) * 4;
     int4 c = make_int4(0, 0, 0, 0);
@@ -197,7 +292,8 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
       int4 o[kMost];
 #pragma unroll
       for (int r = 0; r < kMost; ++r)
-        o[r] = r < C ? *reinterpret_cast<const int4*>(of(counts + b4, r)) : make_int4(0, 0, 0, 0);
+        o[r] = r < (whole ? C : 1) ? *reinterpret_cast<const int4*>(whole ? of(counts + b4, r) : counts + b4)
+                                   : make_int4(0, 0, 0, 0);
 #pragma unroll
       for (int r = 0; r < kMost; ++r) {
         c.x += o[r].x; c.y += o[r].y; c.z += o[r].z; c.w += o[r].w;
@@ -689,6 +785,50 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
     }
   }
   if (CL) cl.sync();   // no CTA leaves while another may still read its shared memory
+  if constexpr (M == kCandidates) {
+    // the last candidates in order, for rest_by_tail: those up to the counter that holds the kPagedTail-th
+    // from the end, ranked against each other
+    if (rank != 0) return;
+    int2* out = tail + (size_t)h * (kPagedTail + 1);
+    const int n_c = bad ? 0 : all[2] + min(need, all[3]), n_t = min(n_c, kPagedTail);
+    if (n_t == 0) {
+      if (tid == 0) out[kPagedTail] = make_int2(0, 0);
+      return;
+    }
+    const int2* ce = cent + (size_t)h * P.cand_len;   // written by the whole cluster, before its sync
+    const uint32_t base_key = T == 0u ? kmin : T, range = kmax - base_key;
+    const int shift = range == 0u ? 0 : max(0, 32 - LB - __clz(range));
+    *reinterpret_cast<int4*>(hist + 4 * tid) = make_int4(0, 0, 0, 0);
+    __syncthreads();
+    for (int i = tid; i < n_c; i += NT)
+      atomicAdd(&hist[(order_key(__int_as_float(__ldcg(&ce[i].y))) - base_key) >> shift], 1);
+    __syncthreads();
+    find_bin(hist, 0, n_c - n_t + 1, wbuf[0], false);
+    const uint64_t end = base_key + (((uint64_t)found_bin + 1u) << shift);   // behind the counter's keys
+    const int m = n_c - found_above;   // candidates up to there
+    if (m > NT) {                      // many alike
+      if (tid == 0) out[kPagedTail] = make_int2(0, 0);
+      return;
+    }
+    if (tid == 0) listed_total = 0;
+    __syncthreads();
+    for (int i = tid; i < n_c; i += NT) {
+      const uint32_t k = order_key(__int_as_float(__ldcg(&ce[i].y)));
+      if (k < end) {
+        const int at = atomicAdd(&listed_total, 1);
+        list[at] = k;
+        every[at] = (uint32_t)i;
+      }
+    }
+    __syncthreads();
+    if (tid < m) {
+      const uint32_t k = list[tid], i = every[tid];
+      int after = 0;
+      for (int o = 0; o < m; ++o) after += list[o] < k || (list[o] == k && every[o] > i);
+      if (after < n_t) out[after] = make_int2((int)k, (int)i);
+    }
+    if (tid == 0) out[kPagedTail] = make_int2(n_t, 0);
+  }
 }
 
 // cap: words of shared memory for keys.
@@ -716,7 +856,8 @@ cudaError_t launch_select_t(const PagedPlan& P, int n_rows, int n, int C, int ca
   return cudaLaunchKernelEx(&cfg, paged_select_kernel<M, NT, SIEVE, CL>, P, ws_ptr<int32_t>(ws, P.off_rows),
                             ws_ptr<int32_t>(ws, P.off_sel), ws_ptr<int2>(ws, P.off_ent),
                             ws_ptr<int32_t>(ws, P.off_crow), ws_ptr<int32_t>(ws, P.off_cand),
-                            ws_ptr<int2>(ws, P.off_cent), ws_ptr<int32_t>(ws, P.off_count),
+                            ws_ptr<int2>(ws, P.off_cent), ws_ptr<int2>(ws, P.off_tail),
+                            ws_ptr<int32_t>(ws, P.off_count),
                             ws_ptr<int32_t>(ws, P.off_status), cap, page_cap, list_cap);
 }
 
