@@ -204,6 +204,14 @@ def test_selection_of_many_long_rows(name):
     assert c.dma.check_device_status(c.p, c.ws) == 0
 
 
+def test_sieve_over_clusters_with_short_rows():
+    # few rows, long enough for clusters of several CTAs each; a short row leaves most of them without a key
+    c = Cache([140_000, 16, 17, 139_999, 20_000], 18, 1, 64, 64, "bf16", 1, seed=33, delta="gate")
+    c.dma.paged_topk(c.p, c.c, c.ws)
+    c.torch.cuda.synchronize()
+    c.check_selection()
+
+
 def test_sieved_row_with_a_bad_page():
     c = Cache([20000] * 12, 16, 1, 64, 64, "bf16", 150, seed=32)
     c.table[3, 200] = -5

@@ -23,6 +23,8 @@
 // order for that (rest_by_tail), and only where they are more is the row counted like any other.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace cg = cooperative_groups;
@@ -32,7 +34,10 @@ namespace {
 
 constexpr int kPsMaxCluster = 8;
 constexpr int kPsGroup = 8;           // sieve: keys of a maximum
-constexpr int kPsMaxBatches = 128;    // 128 groups that a warp reads again together
+constexpr int kPsMaxBatches = 512;    // 32 groups that a warp reads again together
+
+using Yes = std::integral_constant<bool, true>;
+using No = std::integral_constant<bool, false>;
 
 enum SelMode { kRows, kCandidates, kRest };   // a whole row; the prefix, per head; candidates + the rest
 
@@ -265,10 +270,6 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
     if (i + 3 < n) k.w = order_key(f.w);
     return k;
   };
-  // four keys at local index i (a multiple of 4)
-  auto keys4 = [&](int i) -> uint4 {
-    return i < cap ? *reinterpret_cast<const uint4*>(keys + i) : load4(i0 + i);
-  };
   // fn(key) for every key of the stretch, in no particular order
   auto for_keys = [&](auto fn) {
 #pragma unroll 4
@@ -367,7 +368,7 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
   // ---- sieve
   int* index = reinterpret_cast<int*>(keys + list_cap);                       // beside the list's keys
   uint16_t* again = reinterpret_cast<uint16_t*>(keys + 2 * list_cap);         // [list_cap] groups to read again
-  int nb = 0;                                                                 // batches of the list
+  int nb = 0;                                                                 // batches of the list, 512 at most
   if (SIEVE && n >= 2 * kPsGroup * W) {
     float* maxima = reinterpret_cast<float*>(keys);   // where the list will be
     const float nothing = __int_as_float(0x7fffffff);
@@ -446,57 +447,62 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
         }
       }
       __syncthreads();
-      // they are read again, 128 groups (four a lane) together: a place in the list for their keys, written
-      // there in the order of positions (the places of different batches come in any order)
-      nb = many ? 0 : (n_again + 127) >> 7;
-      for (int bt = warp; bt < nb; bt += NW) {
-        float4 f[kU];
-        int from[4];
+      // they are read again, 32 groups (one a lane) together: a place in the list for their keys, written there in
+      // the order of positions (the places of different batches come in any order); a warp has the next batch on
+      // the way while it works on one
+      nb = many ? 0 : (n_again + 31) >> 5;
+      auto fetch = [&](int bt, int& from, float4 (&f)[2]) {
+        const int it = bt * 32 + lane;
+        from = bt < nb && it < n_again ? again[it] * kPsGroup : ns;
+        if (np <= page_cap) {   // as below
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int it = bt * 128 + u * 32 + lane;
-          from[u] = it < n_again ? again[it] * kPsGroup : ns;
-          f[2 * u] = values4(from[u]);
-          f[2 * u + 1] = values4(from[u] + 4);
-        }
-        unsigned own[4];
-        int mine = 0;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float4 a = f[2 * u], c = f[2 * u + 1];
-          own[u] = (unsigned)(a.x >= least) | (unsigned)(a.y >= least) << 1 | (unsigned)(a.z >= least) << 2 |
-                   (unsigned)(a.w >= least) << 3 | (unsigned)(c.x >= least) << 4 | (unsigned)(c.y >= least) << 5 |
-                   (unsigned)(c.z >= least) << 6 | (unsigned)(c.w >= least) << 7;
-          mine += __popc(own[u]);
-        }
-        const int total = __reduce_add_sync(0xffffffffu, mine);
-        int first = 0;
-        if (lane == 0) {
-          first = atomicAdd(&listed_total, total);
-          batch[bt] = make_int2(first, total);
-        }
-        first = __shfl_sync(0xffffffffu, first, 0);
-        if (first + total > list_cap) continue;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int c = __popc(own[u]);
-          int incl = c;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
+          for (int u = 0; u < 2; ++u) {
+            const int pos = i0 + min(from + u * 4, (ns - 1) & ~3);
+            f[u] = *reinterpret_cast<const float4*>(values_of(pages[(pos >> P.page_shift) - tab0]) + (pos & (page - 1)));
           }
+        } else {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) f[u] = values4(from + u * 4);
+        }
+      };
+      int from = ns, from_next;
+      float4 f[2] = {}, f_next[2];
+      if (nb > 0) fetch(warp, from, f);
+      for (int bt = warp; bt < nb; bt += NW) {
+        fetch(bt + NW, from_next, f_next);
+        const int left = ns - from;   // of a whole group 8 or more
+        unsigned own = (unsigned)(f[0].x >= least) | (unsigned)(f[0].y >= least) << 1 | (unsigned)(f[0].z >= least) << 2 |
+                       (unsigned)(f[0].w >= least) << 3 | (unsigned)(f[1].x >= least) << 4 |
+                       (unsigned)(f[1].y >= least) << 5 | (unsigned)(f[1].z >= least) << 6 |
+                       (unsigned)(f[1].w >= least) << 7;
+        if (left < kPsGroup) own &= left > 0 ? (1u << left) - 1u : 0u;
+        const int c = __popc(own);
+        int incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        int first = 0;
+        if (lane == 31) {
+          first = atomicAdd(&listed_total, incl);
+          batch[bt] = make_int2(first, incl);
+        }
+        first = __shfl_sync(0xffffffffu, first, 31);
+        if (first + __shfl_sync(0xffffffffu, incl, 31) <= list_cap) {   // else many keys alike: they do not fit
           int at = first + incl - c;
-          while (own[u] != 0u) {   // nearly always one
-            const int e = __ffs(own[u]) - 1;
-            const float4 q = e < 4 ? f[2 * u] : f[2 * u + 1];
+          while (own != 0u) {   // nearly always one
+            const int e = __ffs(own) - 1;
+            const float4 q = e < 4 ? f[0] : f[1];
             const float v = (e & 3) == 0 ? q.x : (e & 3) == 1 ? q.y : (e & 3) == 2 ? q.z : q.w;
             keys[at] = order_key(v);
-            index[at++] = i0 + from[u] + e;
-            own[u] &= own[u] - 1u;
+            index[at++] = i0 + from + e;
+            own &= own - 1u;
           }
-          first += __shfl_sync(0xffffffffu, incl, 31);
         }
+        from = from_next;
+        f[0] = f_next[0];
+        f[1] = f_next[1];
       }
       __syncthreads();
       items = listed_total;
@@ -529,19 +535,32 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
 
   // ---- read the stretch: keys, smallest, largest, how many
   if (!SIEVE || !sieved) {
-    for (int q0 = tid; q0 * 4 < ns; q0 += NT * kU) {
-      uint4 k[kU];
+    auto keep = [&](int i, const uint4& k) {
+      if (i < cap) *reinterpret_cast<uint4*>(keys + i) = k;
+      note(k.x); note(k.y); note(k.z); note(k.w);
+    };
+    const int jc = M == kRest ? max(0, min(n1p - i0, ns)) : 0;   // candidates come first
+    if (M == kRest)
+      for (int i = tid * 4; i < jc; i += NT * 4) keep(i, load4(i0 + i));
+    if (np <= page_cap) {
+      // every page number at hand: addresses without branches, so that a thread's kU loads leave together
+      for (int q0 = jc + tid * 4; q0 < ns; q0 += NT * 4 * kU) {
+        float4 f[kU];
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int i = (q0 + u * NT) * 4;
-        k[u] = i < ns ? load4(i0 + i) : make_uint4(0u, 0u, 0u, 0u);
-      }
+        for (int u = 0; u < kU; ++u) {
+          const int pos = base + i0 + min(q0 + u * NT * 4, (ns - 1) & ~3) - n1p;
+          f[u] = *reinterpret_cast<const float4*>(values_of(pages[(pos >> P.page_shift) - tab0]) + (pos & (page - 1)));
+        }
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int i = (q0 + u * NT) * 4;
-        if (i < min(ns, cap)) *reinterpret_cast<uint4*>(keys + i) = k[u];
-        note(k[u].x); note(k[u].y); note(k[u].z); note(k[u].w);
+        for (int u = 0; u < kU; ++u) {
+          const int i = q0 + u * NT * 4, left = ns - i;
+          if (left > 0)
+            keep(i, make_uint4(order_key(f[u].x), left > 1 ? order_key(f[u].y) : 0u, left > 2 ? order_key(f[u].z) : 0u,
+                               left > 3 ? order_key(f[u].w) : 0u));
+        }
       }
+    } else {
+      for (int i = jc + tid * 4; i < ns; i += NT * 4) keep(i, load4(i0 + i));
     }
     publish(sh, kmin, kmax, valid);
   }
@@ -645,9 +664,10 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
     if (tid < nb) batch_in[tid] = make_int2(wx.x + incl.x - own.x, wy.x + incl.y - own.y);
     if (tid == 0) cnt[2] = wx.y, cnt[3] = wy.y;   // the CTA's, for the sums over the cluster
   } else if (!bad) {
+    auto count = [&](auto resident) {
 #pragma unroll 4
     for (int j = j0 + lane * 4; j < j1; j += 128) {
-      const uint4 k4 = keys4(j);
+      const uint4 k4 = resident || j < cap ? *reinterpret_cast<const uint4*>(keys + j) : load4(i0 + j);
       const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
       const bool c = M == kRest && i0 + j < n1p;   // n1p and j are multiples of 4
 #pragma unroll
@@ -661,6 +681,9 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
         cnt[3] += c ? 0 : eq;
       }
     }
+    };
+    if (items <= cap) count(Yes());
+    else count(No());
   }
   int2 cta_in = make_int2(0, 0);                // above and at the edge in the CTAs before this one
   int mine[4], tot[4], all[4] = {0, 0, 0, 0};   // before this warp; over the CTA; over the cluster
@@ -739,9 +762,11 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
     int32_t* lp = M == kCandidates ? cand + (size_t)h * P.cand_len : sel + (size_t)row * P.sel_len;
     int2* le = M == kCandidates ? cent + (size_t)h * P.cand_len : ent + (size_t)row * P.sel_len;
     const unsigned lt = (1u << lane) - 1u;
+    auto emit = [&](auto resident) {
     for (int j = j0; j < j1; j += 128) {
       const int jl = j + lane * 4, i = i0 + jl;
-      const uint4 k4 = jl < j1 ? keys4(jl) : make_uint4(0u, 0u, 0u, 0u);
+      uint4 k4 = make_uint4(0u, 0u, 0u, 0u);
+      if (jl < j1) k4 = resident || jl < cap ? *reinterpret_cast<const uint4*>(keys + jl) : load4(i0 + jl);
       const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
       const bool c = M == kRest && i < n1p;
       bool take[4];
@@ -783,6 +808,9 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
           }
       }
     }
+    };
+    if (items <= cap) emit(Yes());
+    else emit(No());
   }
   if (CL) cl.sync();   // no CTA leaves while another may still read its shared memory
   if constexpr (M == kCandidates) {
@@ -876,7 +904,7 @@ cudaError_t launch_select(const PagedPlan& P, int n_rows, int n, void* ws, cudaS
       if (list_cap < seg / (2 * kPsGroup) + 64) list_cap = seg / (2 * kPsGroup) + 64;
       list_cap = (list_cap + 7) & ~7;
       const int cap = 2 * list_cap + list_cap / 2;
-      if (seg <= 65536 && list_cap <= 128 * kPsMaxBatches && cap <= 36864)
+      if (seg <= 65536 && list_cap <= 32 * kPsMaxBatches && cap <= 36864)
         return C > 1 ? launch_select_t<M, 512, true, true>(P, n_rows, n, C, cap, list_cap, ws, s)
                      : launch_select_t<M, 512, true, false>(P, n_rows, n, C, cap, list_cap, ws, s);
     }
