@@ -109,6 +109,34 @@ inline cudaError_t ensure_smem_limit(Kernel k, int bytes) {
   return ensure_smem_limit_impl(reinterpret_cast<const void*>(k), bytes);
 }
 
+// Programmatic dependent launch.  A kernel launched with launch_after may start while the one in front of it
+// in the stream still runs, once that one's blocks have all called pdl_trigger (or ended); it calls pdl_wait,
+// in every thread that reads or writes global memory, before it does so: from there on all that came before
+// is complete.  What precedes pdl_wait (and the launch itself) then costs no time of its own.
+DMA_DEVINL void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+DMA_DEVINL void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// cluster: CTAs of a cluster along x (1: none).
+template <typename... Params, typename... Args>
+inline cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int block, size_t smem, cudaStream_t s,
+                                int cluster, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

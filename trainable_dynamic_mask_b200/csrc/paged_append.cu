@@ -86,7 +86,7 @@ struct SlotDest {
   }
   DMA_DEVINL size_t step(int part) const { return part == 0 ? (size_t)P.d : (size_t)P.d << P.page_shift; }
   DMA_DEVINL void finish() const {
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // the gate kernel in front is done too
+    pdl_wait();   // the gate kernel in front is done too
   }
 };
 
@@ -114,7 +114,7 @@ DMA_DEVINL void gate_places(const PagedPlan& P, const PagedAppendArgs& a, int t0
 template <int HT>   // column tiles of 8 heads
 __global__ void __launch_bounds__(kAgThreads)
 paged_gate_mma_kernel(PagedPlan P, PagedAppendArgs a, int32_t* status) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_trigger();
   extern __shared__ __align__(128) unsigned char sm[];
   __shared__ long long where[kAgTok];
   const int K = P.Hkv * P.d, KC = K / 8, dch = P.d / 8;
@@ -198,7 +198,7 @@ constexpr int kAfK = 512;      // channels staged at a time
 template <typename T>
 __global__ void __launch_bounds__(kAgThreads)
 paged_gate_kernel(PagedPlan P, PagedAppendArgs a, int HP, int32_t* status) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_trigger();
   extern __shared__ __align__(16) float fsm[];
   __shared__ long long where[kAfTok];
   float* Vs = fsm;                   // [kAfK][kAfTok]

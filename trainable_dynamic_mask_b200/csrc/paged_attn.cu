@@ -84,6 +84,8 @@ paged_list_kernel(const T* __restrict__ Q, const T* __restrict__ K, const T* __r
   __shared__ int last;
   const int row = blockIdx.y, h = row % H, g = h / (H / Hkv);
   const int tid = threadIdx.x, lane = tid & 31, grp = tid / L, e = (lane % L) * 8;
+  pdl_trigger();
+  pdl_wait();
   const int count = min(rows[row].x, sel_len);
   const int k0 = blockIdx.x * kPagedSplit, nk = min(count - k0, kPagedSplit);
   if (nk <= 0 && blockIdx.x > 0) return;   // the first CTA of a row works even if there is nothing
@@ -277,6 +279,8 @@ paged_cand_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ K
   const int h = blockIdx.y, g = h / (H / Hkv), s0 = blockIdx.z * 16 * R;
   const int rg = warp / KG, kg = warp % KG;
   const int c0 = blockIdx.x * cand_split;
+  pdl_trigger();
+  pdl_wait();
   const int nc = max(0, min(crow[h], min(cand_len, c0 + cand_split)) - c0);
   const int nt = (nc + kPcTile - 1) / kPcTile;
   for (int i = tid; i < nt * kPcTile; i += kPcThreads) {
@@ -489,11 +493,11 @@ template <int D, int R>
 cudaError_t launch_cand(const PagedPlan& P, const void* Q, void* ws, cudaStream_t s) {
   const cudaError_t e = ensure_smem_limit(paged_cand_kernel<D, R>, cand_smem<D>());
   if (e != cudaSuccess) return e;
-  paged_cand_kernel<D, R><<<dim3(P.n_psplit, P.H, (P.B + 16 * R - 1) / (16 * R)), cand_threads<R>(), cand_smem<D>(), s>>>(
+  return launch_after(
+      paged_cand_kernel<D, R>, dim3(P.n_psplit, P.H, (P.B + 16 * R - 1) / (16 * R)), cand_threads<R>(), cand_smem<D>(), s, 1,
       (const uint16_t*)Q, (const uint16_t*)P.K, (const uint16_t*)P.V, ws_ptr<int4>(ws, P.off_rows),
       ws_ptr<int32_t>(ws, P.off_crow), ws_ptr<int2>(ws, P.off_cent), ws_ptr<float>(ws, P.off_part), P.B, P.H, P.Hkv,
       P.page_shift, P.cand_len, P.cand_split, P.n_psplit + P.n_split, P.scale);
-  return cudaGetLastError();
 }
 
 template <int D>
@@ -507,11 +511,10 @@ template <typename T, int D, int NT>
 cudaError_t launch_list_t(const PagedPlan& P, const void* Q, void* ws, void* O, float* LSE, cudaStream_t s) {
   const cudaError_t e = ensure_smem_limit(paged_list_kernel<T, D, NT>, list_smem<T, NT>());
   if (e != cudaSuccess) return e;
-  paged_list_kernel<T, D, NT><<<dim3(P.n_split, P.B * P.H), NT, list_smem<T, NT>(), s>>>(
-      (const T*)Q, (const T*)P.K, (const T*)P.V, ws_ptr<int4>(ws, P.off_rows), ws_ptr<int2>(ws, P.off_ent),
+  return launch_after(
+      paged_list_kernel<T, D, NT>, dim3(P.n_split, P.B * P.H), NT, list_smem<T, NT>(), s, 1, (const T*)Q, (const T*)P.K, (const T*)P.V, ws_ptr<int4>(ws, P.off_rows), ws_ptr<int2>(ws, P.off_ent),
       ws_ptr<float>(ws, P.off_part), ws_ptr<int32_t>(ws, P.off_count), (T*)O, LSE, P.H, P.Hkv, P.page_shift, P.sel_len,
       P.n_split, P.n_psplit, P.scale);
-  return cudaGetLastError();
 }
 
 template <typename T, int D>

@@ -181,6 +181,8 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
   auto of = [&](auto* p, int r) { return CL ? cl.map_shared_rank(p, r) : p; };
   const int row = blockIdx.y, h = M == kCandidates ? row : row % P.H, b = M == kCandidates ? 0 : row / P.H;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_trigger();
+  pdl_wait();
   const int W = row_window(P.w_heads, h, P.H, P.w);
   const int page = 1 << P.page_shift;
   const int32_t* tab = P.table + (size_t)b * P.max_pages;
@@ -869,24 +871,8 @@ cudaError_t launch_select_t(const PagedPlan& P, int n_rows, int n, int C, int ca
   const size_t smem = (size_t)(cap + page_cap) * 4;
   const cudaError_t e = ensure_smem_limit(paged_select_kernel<M, NT, SIEVE, CL>, (int)smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(C, n_rows);
-  cfg.blockDim = dim3(NT);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = CL ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, paged_select_kernel<M, NT, SIEVE, CL>, P, ws_ptr<int32_t>(ws, P.off_rows),
-                            ws_ptr<int32_t>(ws, P.off_sel), ws_ptr<int2>(ws, P.off_ent),
-                            ws_ptr<int32_t>(ws, P.off_crow), ws_ptr<int32_t>(ws, P.off_cand),
-                            ws_ptr<int2>(ws, P.off_cent), ws_ptr<int2>(ws, P.off_tail),
-                            ws_ptr<int32_t>(ws, P.off_count),
-                            ws_ptr<int32_t>(ws, P.off_status), cap, page_cap, list_cap);
+  return launch_after(paged_select_kernel<M, NT, SIEVE, CL>, dim3(C, n_rows), NT, smem, s, CL ? C : 1,
+                      P, ws_ptr<int32_t>(ws, P.off_rows), ws_ptr<int32_t>(ws, P.off_sel), ws_ptr<int2>(ws, P.off_ent), ws_ptr<int32_t>(ws, P.off_crow), ws_ptr<int32_t>(ws, P.off_cand), ws_ptr<int2>(ws, P.off_cent), ws_ptr<int2>(ws, P.off_tail), ws_ptr<int32_t>(ws, P.off_count), ws_ptr<int32_t>(ws, P.off_status), cap, page_cap, list_cap);
 }
 
 // Launches the selection of `n_rows` rows of at most n values.

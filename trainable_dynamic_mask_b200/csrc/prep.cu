@@ -54,7 +54,7 @@ prep_bwd_kernel(const __grid_constant__ PrepArgs a, int wt) {
   __shared__ uint64_t rate[D / 2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grp = lane / L, e = (lane % L) * 8;
   const bool upper = e >= a.rot >> 1;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_trigger();
   for (int k = tid; k < a.rot >> 1; k += kRwThreads) rate[k] = turn_rate(__ldg(a.inv_freq + k));
   if (lane < kTabPad) tab[warp][D / 2 + lane] = make_float2(1.f, 0.f);
   __syncthreads();
@@ -172,7 +172,7 @@ prep_reduce_kernel(const float* __restrict__ part, float* __restrict__ dq_weight
   __shared__ double red[32][8];
   const int tid = threadIdx.x, c = blockIdx.x * 8 + (tid & 7), w = tid >> 3;
   float* out = blockIdx.y == 0 ? dq_weight : dk_weight;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_wait();
   if (out == nullptr) return;
   const float* p = part + (size_t)blockIdx.y * n_blocks * D + c;
   double v = 0.0;
@@ -211,16 +211,7 @@ cudaError_t launch_bwd(const PrepArgs& a, float* dqw, float* dkw, cudaStream_t s
   kernel<<<blocks, kRwThreads, BwdRing<T>::kBytes, s>>>(a, wt);
   e = cudaGetLastError();
   if (e != cudaSuccess || (dqw == nullptr && dkw == nullptr)) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(D / 8, 2);
-  cfg.blockDim = dim3(1024);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prep_reduce_kernel, (const float*)a.part, dqw, dkw, blocks, D);
+  return launch_after(prep_reduce_kernel, dim3(D / 8, 2), 1024, 0, s, 1, (const float*)a.part, dqw, dkw, blocks, D);
 }
 
 }  // namespace

@@ -348,20 +348,12 @@ template <typename T, int D, typename Dest>
 cudaError_t launch_row_walk(const PrepArgs& a, const Dest& dest, bool dependent, cudaStream_t s) {
   int wt;
   const int blocks = walk_blocks((long long)a.B * a.N, 3, &wt);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(kRwThreads);
-  cfg.dynamicSmemBytes = FwdRing<T>::kBytes;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = dependent ? 1 : 0;
   auto kernel = a.inter ? row_walk_kernel<T, D, true, Dest> : row_walk_kernel<T, D, false, Dest>;
   const cudaError_t e = ensure_smem_limit(kernel, FwdRing<T>::kBytes);
   if (e != cudaSuccess) return e;
-  return cudaLaunchKernelEx(&cfg, kernel, a, dest, wt);
+  if (dependent) return launch_after(kernel, dim3(blocks), kRwThreads, FwdRing<T>::kBytes, s, 1, a, dest, wt);
+  kernel<<<blocks, kRwThreads, FwdRing<T>::kBytes, s>>>(a, dest, wt);
+  return cudaGetLastError();
 }
 
 }  // namespace dma
