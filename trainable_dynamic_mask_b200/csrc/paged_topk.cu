@@ -64,6 +64,9 @@ template <int NW> DMA_DEVINL int2 warps_before(int x, int* buf) {
   return make_int2(__shfl_sync(0xffffffffu, v - own, warp), __shfl_sync(0xffffffffu, v, NW - 1));
 }
 
+// Sorts the last in the order of selection (small key, then high position) first.
+DMA_DEVINL uint64_t last_first(uint32_t key, uint32_t position) { return (uint64_t)key << 32 | (uint32_t)~position; }
+
 // A row's selection where all w candidates would fill it and at most kPagedTail - 1 of its own keys pass the
 // last of them: each of those m keys and of the last m candidates is in unless m of these 2 m come after it.
 // keys, where: room for kPagedTail; false (for the whole block): not that simple, nothing written.
@@ -123,10 +126,9 @@ DMA_DEVINL bool rest_by_tail(const PagedPlan& P, const int32_t* tab, int h, int 
   int after = 0;
   if (tid < m) {
     const uint32_t k = keys[tid];
-    for (int i = 0; i < m; ++i) {
-      after += keys[i] < k || (keys[i] == k && i > tid);
-      after += (uint32_t)tail[i].x < k;
-    }
+#pragma unroll 4
+    for (int i = 0; i < m; ++i)
+      after += (int)(last_first(keys[i], i) < last_first(k, tid)) + (int)((uint32_t)tail[i].x < k);
   } else if (tid >= 64 && tid < 64 + m) {
     const uint32_t k = (uint32_t)tail[tid - 64].x;
     after = tid - 64;
@@ -285,9 +287,9 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
     }
   };
 
-  // the counter (of 4 NT, summed over the cluster if whole) that holds the want-th largest key, `above` keys lying
+  // the counter (of 4 NT, summed over the cluster) that holds the want-th largest key, `above` keys lying
   // above all of them: found_bin, found_above, found_count
-  auto find_bin = [&](int* counts, int above, int want, int* buf, bool whole = true) {
+  auto find_bin = [&](int* counts, int above, int want, int* buf) {
     // thread t sums counters 4 t' .. 4 t' + 3, t' = NT - 1 - t: from the top
     const int b4 = (NT - 1 - tid) * 4;
     int4 c = make_int4(0, 0, 0, 0);
@@ -295,8 +297,7 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
       int4 o[kMost];
 #pragma unroll
       for (int r = 0; r < kMost; ++r)
-        o[r] = r < (whole ? C : 1) ? *reinterpret_cast<const int4*>(whole ? of(counts + b4, r) : counts + b4)
-                                   : make_int4(0, 0, 0, 0);
+        o[r] = r < C ? *reinterpret_cast<const int4*>(of(counts + b4, r)) : make_int4(0, 0, 0, 0);
 #pragma unroll
       for (int r = 0; r < kMost; ++r) {
         c.x += o[r].x; c.y += o[r].y; c.z += o[r].z; c.w += o[r].w;
@@ -573,7 +574,8 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
 
   // ---- the edge T: keys above it are in, `need` of those equal to it, lowest positions first
   uint32_t T = 0u;
-  int need = 0;
+  int need = 0, tail_n = 0;
+  uint64_t tail_end = 0u;   // candidates: the last ones' keys are below it, tail_n of them (0: not looked for)
   if (!bad && valid > W) {
     uint32_t lo = kmin, span = 0xffffffffu;   // the edge lies in [lo, lo + span]
     int above = 0;                            // keys above that interval
@@ -586,6 +588,23 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
       });
       all_sync();
       find_bin(hist, above, W, wbuf[0]);
+      if constexpr (M == kCandidates) {
+        if (tail_end == 0u) {
+          // the counter of the kPagedTail-th key from the edge: the last candidates are those below its end
+          const int bin = found_bin, up = found_above, here = found_count;
+          __syncthreads();
+          find_bin(hist, 0, max(1, W - kPagedTail + 1), wbuf[0]);
+          tail_n = W - found_above;
+          tail_end = lo + (((uint64_t)found_bin + 1u) << shift);
+          __syncthreads();
+          if (tid == 0) {
+            found_bin = bin;
+            found_above = up;
+            found_count = here;
+          }
+          __syncthreads();
+        }
+      }
       above = found_above;
       lo += (uint32_t)found_bin << shift;
       T = lo;
@@ -806,6 +825,11 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
           if (take[u]) {
             lp[at] = pos + u;
             le[at] = make_int2(slot + u, (int)((k[u] & 0x80000000u) ? k[u] ^ 0x80000000u : ~k[u]));
+            if (M == kCandidates && tail_n <= NT && k[u] < tail_end) {
+              const int i = atomicAdd(of(&listed_total, 0), 1);   // in any order: they are ranked below
+              of(list, 0)[i] = k[u];
+              of(every, 0)[i] = (uint32_t)at;
+            }
             ++at;
           }
       }
@@ -816,45 +840,17 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
   }
   if (CL) cl.sync();   // no CTA leaves while another may still read its shared memory
   if constexpr (M == kCandidates) {
-    // the last candidates in order, for rest_by_tail: those up to the counter that holds the kPagedTail-th
-    // from the end, ranked against each other
+    // the last candidates in order, for rest_by_tail
+    if (!CL) __syncthreads();
     if (rank != 0) return;
     int2* out = tail + (size_t)h * (kPagedTail + 1);
-    const int n_c = bad ? 0 : all[2] + min(need, all[3]), n_t = min(n_c, kPagedTail);
-    if (n_t == 0) {
-      if (tid == 0) out[kPagedTail] = make_int2(0, 0);
-      return;
-    }
-    const int2* ce = cent + (size_t)h * P.cand_len;   // written by the whole cluster, before its sync
-    const uint32_t base_key = T == 0u ? kmin : T, range = kmax - base_key;
-    const int shift = range == 0u ? 0 : max(0, 32 - LB - __clz(range));
-    *reinterpret_cast<int4*>(hist + 4 * tid) = make_int4(0, 0, 0, 0);
-    __syncthreads();
-    for (int i = tid; i < n_c; i += NT)
-      atomicAdd(&hist[(order_key(__int_as_float(__ldcg(&ce[i].y))) - base_key) >> shift], 1);
-    __syncthreads();
-    find_bin(hist, 0, n_c - n_t + 1, wbuf[0], false);
-    const uint64_t end = base_key + (((uint64_t)found_bin + 1u) << shift);   // behind the counter's keys
-    const int m = n_c - found_above;   // candidates up to there
-    if (m > NT) {                      // many alike
-      if (tid == 0) out[kPagedTail] = make_int2(0, 0);
-      return;
-    }
-    if (tid == 0) listed_total = 0;
-    __syncthreads();
-    for (int i = tid; i < n_c; i += NT) {
-      const uint32_t k = order_key(__int_as_float(__ldcg(&ce[i].y)));
-      if (k < end) {
-        const int at = atomicAdd(&listed_total, 1);
-        list[at] = k;
-        every[at] = (uint32_t)i;
-      }
-    }
-    __syncthreads();
+    const int m = bad ? 0 : listed_total, n_t = min(m, kPagedTail);
     if (tid < m) {
       const uint32_t k = list[tid], i = every[tid];
+      const uint64_t mine_last = last_first(k, i);
       int after = 0;
-      for (int o = 0; o < m; ++o) after += list[o] < k || (list[o] == k && every[o] > i);
+#pragma unroll 8
+      for (int o = 0; o < m; ++o) after += last_first(list[o], every[o]) < mine_last;
       if (after < n_t) out[after] = make_int2((int)k, (int)i);
     }
     if (tid == 0) out[kPagedTail] = make_int2(n_t, 0);
