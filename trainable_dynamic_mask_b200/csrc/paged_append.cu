@@ -2,10 +2,11 @@
 // values delta = exp(A softplus(v Delta)) formed from the values on the way, queries of the same tokens
 // normed and rotated.
 //
-// Two kernels that run side by side: the gate's product (the values of 16 tokens against Delta, tensor
-// cores for bf16) and the walk over the rows (rows.cuh, as in prep.cu).  The second is launched as a
+// Two kernels that run side by side: the walk over the rows (rows.cuh, as in prep.cu) and the gate's product
+// (the values of 16 tokens against Delta, tensor cores for bf16).  The second is launched as a
 // programmatic dependent of the first, which lets it go at once; it waits for the first only before it
-// ends, so that whatever follows in the stream finds both done.
+// ends, so that whatever follows in the stream finds both done.  The rows' shares of the work are fixed when
+// they start and theirs is the longer way, so they come first.
 #include "rows.cuh"
 
 namespace dma {
@@ -52,6 +53,7 @@ DMA_DEVINL Place place_of(const PagedPlan& P, const PagedAppendArgs& a, int t, i
 // Keys and values to their slots, queries to Q [T, H, D].  A warp looks up the places of its next 32 tokens
 // together, a token a lane: the lookups' three or more dependent reads are then paid once.
 struct SlotDest {
+  static constexpr int kDepth = 4, kPerSm = 2;   // two CTAs an SM leave the registers for the gate
   struct Token {
     int position;
     unsigned tok;
@@ -85,9 +87,6 @@ struct SlotDest {
     return (part == 1 ? P.K : P.V) + t.slot * P.d * size;
   }
   DMA_DEVINL size_t step(int part) const { return part == 0 ? (size_t)P.d : (size_t)P.d << P.page_shift; }
-  DMA_DEVINL void finish() const {
-    pdl_wait();   // the gate kernel in front is done too
-  }
 };
 
 // ---------------------------------------------------------------- gate, tensor cores
@@ -107,66 +106,85 @@ DMA_DEVINL void gate_places(const PagedPlan& P, const PagedAppendArgs& a, int t0
   }
 }
 
-// x [16 tokens, H] = v [16, K] Delta [K, H], K = Hkv d: the warps split K in steps of 16 and their tiles
-// are summed through shared memory (in a fixed order).  bf16 products are exact in float32, in which all
-// is accumulated.  Everything the CTA reads is in flight before the first wait: one trip to memory is
-// what bounds a decode step.
+constexpr int kAgK = 256;         // channels of a stage, two stages
+
+template <int HT> constexpr int gate_smem() {
+  constexpr int stages = 2 * kAgK * (kAgTok + 8 * HT) * 2, sums = kAgWarps * kAgTok * 8 * HT * 4;
+  return stages > sums ? stages : sums;
+}
+
+// x [16 tokens, H] = v [16, K] Delta [K, H], K = Hkv d, in stages of 256 channels: the warps split a stage in
+// steps of 16 and their tiles are summed through shared memory (in a fixed order).  bf16 products are exact
+// in float32, in which all is accumulated.  Two stages (32 to 80 KB) rather than all of K at once leave
+// room for the rows' CTAs beside these.
 template <int HT>   // column tiles of 8 heads
 __global__ void __launch_bounds__(kAgThreads)
-paged_gate_mma_kernel(PagedPlan P, PagedAppendArgs a, int32_t* status) {
-  pdl_trigger();
+paged_gate_mma_kernel(const __grid_constant__ PagedPlan P, const __grid_constant__ PagedAppendArgs a, int32_t* status) {
   extern __shared__ __align__(128) unsigned char sm[];
   __shared__ long long where[kAgTok];
-  const int K = P.Hkv * P.d, KC = K / 8, dch = P.d / 8;
-  uint16_t* Vs = reinterpret_cast<uint16_t*>(sm);                   // [16][K], chunk c of row r at c ^ (r & 7)
-  uint16_t* Ds = Vs + kAgTok * K;                                   // [K][8 HT]
-  float* red = reinterpret_cast<float*>(Ds + (size_t)K * 8 * HT);   // [8 warps][16][8 HT]
+  constexpr int KC = kAgK / 8, kStage = kAgK * (kAgTok + 8 * HT);   // elements
+  uint16_t* const stage = reinterpret_cast<uint16_t*>(sm);   // [2]: v [16][256], chunk c of row r at c ^ (r & 7);
+                                                             // Delta [256][8 HT]
+  float* red = reinterpret_cast<float*>(sm);                 // [8 warps][16][8 HT], in the stages' place
+  const int K = P.Hkv * P.d, dch = P.d / 8, n_st = (K + kAgK - 1) / kAgK;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int t0 = blockIdx.x * kAgTok;
   const uint16_t* v = static_cast<const uint16_t*>(a.v);
   const uint16_t* Delta = static_cast<const uint16_t*>(a.Delta);
-  for (int u = tid; u < kAgTok * KC; u += kAgThreads) {
-    const int r = u / KC, kc = u % KC, g = kc / dch, c = kc % dch;
-    const bool in = t0 + r < a.T;
-    const uint16_t* src = in ? v + (long long)(t0 + r) * a.st.v[1] + g * a.st.v[2] + c * 8 : v;
-    cp_async_16(smem_u32(Vs + (size_t)r * K + ((kc ^ (r & 7)) * 8)), src, in ? 16 : 0);
-  }
-  if ((P.H & 7) == 0) {
-    const int hc = P.H / 8;
-    for (int u = tid; u < K * HT; u += kAgThreads) {
-      const int r = u / HT, c = u % HT;
-      const bool in = c < hc;
-      cp_async_16(smem_u32(Ds + (size_t)r * 8 * HT + c * 8), in ? Delta + (size_t)r * P.H + c * 8 : Delta, in ? 16 : 0);
+  auto load = [&](int st) {
+    uint16_t* Vs = stage + (st & 1) * kStage;
+    uint16_t* Ds = Vs + kAgTok * kAgK;
+#pragma unroll
+    for (int u = tid; u < kAgTok * KC; u += kAgThreads) {
+      const int r = u / KC, kc = u % KC, q = st * KC + kc, g = q / dch, c = q - g * dch;
+      const bool in = t0 + r < a.T && q * 8 < K;
+      const uint16_t* src = in ? v + (long long)(t0 + r) * a.st.v[1] + g * a.st.v[2] + c * 8 : v;
+      cp_async_16(smem_u32(Vs + r * kAgK + ((kc ^ (r & 7)) * 8)), src, in ? 16 : 0);
     }
-  } else {
-    for (int u = tid; u < K * 8 * HT; u += kAgThreads) {
-      const int r = u / (8 * HT), h = u % (8 * HT);
-      Ds[u] = h < P.H ? Delta[(size_t)r * P.H + h] : (uint16_t)0;
+    if ((P.H & 7) == 0) {
+      const int hc = P.H / 8;
+#pragma unroll
+      for (int u = tid; u < kAgK * HT; u += kAgThreads) {
+        const int r = u / HT, c = u % HT, k = st * kAgK + r;
+        const bool in = c < hc && k < K;
+        cp_async_16(smem_u32(Ds + r * 8 * HT + c * 8), in ? Delta + (size_t)k * P.H + c * 8 : Delta, in ? 16 : 0);
+      }
+    } else {
+      for (int u = tid; u < kAgK * 8 * HT; u += kAgThreads) {
+        const int r = u / (8 * HT), h = u % (8 * HT), k = st * kAgK + r;
+        Ds[u] = h < P.H && k < K ? Delta[(size_t)k * P.H + h] : (uint16_t)0;
+      }
     }
-  }
-  cp_async_commit();
+    cp_async_commit();
+  };
+  load(0);
   gate_places(P, a, t0, kAgTok, where, status);
-  cp_async_wait<0>();
-  __syncthreads();
   float acc[HT][4];
 #pragma unroll
   for (int n = 0; n < HT; ++n)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-  const uint32_t vs = smem_u32(Vs), ds = smem_u32(Ds);
-  const int arow = lane & 15, achunk = lane >> 4;
-  const int brow = lane & 15, btile = lane >> 4;
-  for (int ks = warp; ks < K / 16; ks += kAgWarps) {
-    uint32_t f[4];
-    const int kc = ks * 2 + achunk;
-    ldmatrix_x4(vs + (uint32_t)(arow * K + ((kc ^ (arow & 7)) * 8)) * 2, f[0], f[1], f[2], f[3]);
+  const int arow = lane & 15, half = lane >> 4;
+  for (int st = 0; st < n_st; ++st) {
+    if (st + 1 < n_st) load(st + 1);
+    else cp_async_commit();
+    cp_async_wait<1>();
+    __syncthreads();
+    const uint32_t vs = smem_u32(stage + (st & 1) * kStage), ds = vs + kAgTok * kAgK * 2;
 #pragma unroll
-    for (int n = 0; n < HT; n += 2) {
-      uint32_t b0, b1, b2, b3;
-      ldmatrix_x4_trans(ds + (uint32_t)((ks * 16 + brow) * 8 * HT + (n + btile) * 8) * 2, b0, b1, b2, b3);
-      mma_bf16_16816(acc[n], f, b0, b1);
-      mma_bf16_16816(acc[n + 1], f, b2, b3);
+    for (int i = 0; i < kAgK / 16 / kAgWarps; ++i) {
+      const int ks = warp + i * kAgWarps;
+      uint32_t f[4];
+      ldmatrix_x4(vs + (uint32_t)(arow * kAgK + (((ks * 2 + half) ^ (arow & 7)) * 8)) * 2, f[0], f[1], f[2], f[3]);
+#pragma unroll
+      for (int n = 0; n < HT; n += 2) {
+        uint32_t b0, b1, b2, b3;
+        ldmatrix_x4_trans(ds + (uint32_t)((ks * 16 + arow) * 8 * HT + (n + half) * 8) * 2, b0, b1, b2, b3);
+        mma_bf16_16816(acc[n], f, b0, b1);
+        mma_bf16_16816(acc[n + 1], f, b2, b3);
+      }
     }
+    __syncthreads();   // the stage may be filled again
   }
   const int g = lane >> 2, q = lane & 3;
 #pragma unroll
@@ -186,19 +204,18 @@ paged_gate_mma_kernel(PagedPlan P, PagedAppendArgs a, int32_t* status) {
     for (int w = 0; w < kAgWarps; ++w) x += red[((size_t)w * kAgTok + t) * 8 * HT + h];
     P.delta[at + ((long long)h << P.page_shift)] = expf(a.A[h] * softplus_of(x));
   }
+  pdl_wait();   // the rows' kernel in front is done too
 }
 
-// ---------------------------------------------------------------- gate, any type and width
+// ---------------------------------------------------------------- gate, float32
 
 constexpr int kAfTok = 8;      // tokens of a CTA
 constexpr int kAfK = 512;      // channels staged at a time
 
-// float32 storage (and bf16 rows too wide for the kernel above): the same product on the FMA pipe.
-// Thread = one head and one of NS slices of the staged channels, for 8 tokens.
-template <typename T>
+// float32 storage: the same product on the FMA pipe, with the values' full precision.  Thread = one head and
+// one of NS slices of the staged channels, for 8 tokens.
 __global__ void __launch_bounds__(kAgThreads)
-paged_gate_kernel(PagedPlan P, PagedAppendArgs a, int HP, int32_t* status) {
-  pdl_trigger();
+paged_gate_kernel(const __grid_constant__ PagedPlan P, const __grid_constant__ PagedAppendArgs a, int HP, int32_t* status) {
   extern __shared__ __align__(16) float fsm[];
   __shared__ long long where[kAfTok];
   float* Vs = fsm;                   // [kAfK][kAfTok]
@@ -206,8 +223,8 @@ paged_gate_kernel(PagedPlan P, PagedAppendArgs a, int HP, int32_t* status) {
   const int K = P.Hkv * P.d, NS = kAgThreads / HP;
   const int tid = threadIdx.x, h = tid % HP, sl = tid / HP;
   const int t0 = blockIdx.x * kAfTok;
-  const T* v = static_cast<const T*>(a.v);
-  const T* Delta = static_cast<const T*>(a.Delta);
+  const float* v = static_cast<const float*>(a.v);
+  const float* Delta = static_cast<const float*>(a.Delta);
   gate_places(P, a, t0, kAfTok, where, status);
   float acc[kAfTok];
 #pragma unroll
@@ -218,13 +235,13 @@ paged_gate_kernel(PagedPlan P, PagedAppendArgs a, int HP, int32_t* status) {
     for (int u = tid; u < kn * kAfTok; u += kAgThreads) {
       const int t = u / kn, kk = u % kn, g = (k0 + kk) / P.d, c = (k0 + kk) % P.d;
       Vs[kk * kAfTok + t] =
-          t0 + t < a.T ? load_as_f32(v + (long long)(t0 + t) * a.st.v[1] + g * a.st.v[2] + c) : 0.f;
+          t0 + t < a.T ? v[(long long)(t0 + t) * a.st.v[1] + g * a.st.v[2] + c] : 0.f;
     }
     __syncthreads();
     if (h < P.H && sl < NS) {
 #pragma unroll 4
       for (int kk = sl; kk < kn; kk += NS) {
-        const float dl = load_as_f32(Delta + (size_t)(k0 + kk) * P.H + h);
+        const float dl = Delta[(size_t)(k0 + kk) * P.H + h];
         const float4 v0 = reinterpret_cast<const float4*>(Vs + kk * kAfTok)[0];
         const float4 v1 = reinterpret_cast<const float4*>(Vs + kk * kAfTok)[1];
         acc[0] = fmaf(v0.x, dl, acc[0]); acc[1] = fmaf(v0.y, dl, acc[1]);
@@ -247,34 +264,26 @@ paged_gate_kernel(PagedPlan P, PagedAppendArgs a, int HP, int32_t* status) {
     for (int s = 0; s < NS; ++s) x += red[(s * kAfTok + t) * HP + hh];
     P.delta[at + ((long long)hh << P.page_shift)] = expf(a.A[hh] * softplus_of(x));
   }
+  pdl_wait();   // the rows' kernel in front is done too
 }
 
 template <int HT>
-cudaError_t launch_gate_mma(const PagedPlan& P, const PagedAppendArgs& a, size_t smem, int32_t* status, cudaStream_t s) {
-  const cudaError_t e = ensure_smem_limit(paged_gate_mma_kernel<HT>, (int)smem);
+cudaError_t launch_gate_mma(const PagedPlan& P, const PagedAppendArgs& a, int32_t* status, cudaStream_t s) {
+  const cudaError_t e = ensure_smem_limit(paged_gate_mma_kernel<HT>, gate_smem<HT>());
   if (e != cudaSuccess) return e;
-  paged_gate_mma_kernel<HT><<<(a.T + kAgTok - 1) / kAgTok, kAgThreads, smem, s>>>(P, a, status);
-  return cudaGetLastError();
+  return launch_after(paged_gate_mma_kernel<HT>, dim3((a.T + kAgTok - 1) / kAgTok), kAgThreads, gate_smem<HT>(), s, 1, P, a,
+                      status);
 }
 
 cudaError_t launch_gate(const PagedPlan& P, const PagedAppendArgs& a, int32_t* status, cudaStream_t s) {
-  const size_t K = (size_t)P.Hkv * P.d;
-  if (P.bf16) {
-    const int HT = P.H <= 16 ? 2 : P.H <= 32 ? 4 : 8;
-    const size_t smem = kAgTok * K * 2 + K * 8 * HT * 2 + (size_t)kAgWarps * kAgTok * 8 * HT * 4;
-    if (smem <= 200 * 1024)   // else the rows do not fit (more than about 2700 channels at 32 heads)
-      return HT == 2   ? launch_gate_mma<2>(P, a, smem, status, s)
-             : HT == 4 ? launch_gate_mma<4>(P, a, smem, status, s)
-                       : launch_gate_mma<8>(P, a, smem, status, s);
-  }
+  if (P.bf16)
+    return P.H <= 16   ? launch_gate_mma<2>(P, a, status, s)
+           : P.H <= 32 ? launch_gate_mma<4>(P, a, status, s)
+                       : launch_gate_mma<8>(P, a, status, s);
   const int HP = P.H <= 16 ? 16 : P.H <= 32 ? 32 : 64;
   const int smem = (kAfK * kAfTok + kAgThreads * kAfTok) * (int)sizeof(float);
   const int blocks = (a.T + kAfTok - 1) / kAfTok;
-  if (P.bf16)
-    paged_gate_kernel<uint16_t><<<blocks, kAgThreads, smem, s>>>(P, a, HP, status);
-  else
-    paged_gate_kernel<float><<<blocks, kAgThreads, smem, s>>>(P, a, HP, status);
-  return cudaGetLastError();
+  return launch_after(paged_gate_kernel, dim3(blocks), kAgThreads, smem, s, 1, P, a, HP, status);
 }
 
 template <typename T, int D>
@@ -298,18 +307,19 @@ cudaError_t launch_rows(const PagedPlan& P, const PagedAppendArgs& a, int32_t* s
   d.a = a;
   d.status = status;
   d.size = (int)sizeof(T);
-  return launch_row_walk<T, D>(w, d, true, s);
+  return launch_row_walk<T, D>(w, d, s);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_append(const PagedPlan& P, const PagedAppendArgs& a, void* ws, cudaStream_t s) {
   int32_t* status = ws_ptr<int32_t>(ws, P.off_status);
-  const cudaError_t e = launch_gate(P, a, status, s);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
   if (P.bf16)
-    return P.d == 128 ? launch_rows<uint16_t, 128>(P, a, status, s) : launch_rows<uint16_t, 64>(P, a, status, s);
-  return P.d == 128 ? launch_rows<float, 128>(P, a, status, s) : launch_rows<float, 64>(P, a, status, s);
+    e = P.d == 128 ? launch_rows<uint16_t, 128>(P, a, status, s) : launch_rows<uint16_t, 64>(P, a, status, s);
+  else
+    e = P.d == 128 ? launch_rows<float, 128>(P, a, status, s) : launch_rows<float, 64>(P, a, status, s);
+  return e == cudaSuccess ? launch_gate(P, a, status, s) : e;
 }
 
 }  // namespace dma

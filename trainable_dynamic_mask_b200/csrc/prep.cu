@@ -17,6 +17,7 @@ namespace {
 
 // Dense outputs [B, heads, N, D].
 struct DenseDest {
+  static constexpr int kDepth = 4, kPerSm = 3;
   struct Token {
     int position;
     unsigned b, n;
@@ -35,7 +36,6 @@ struct DenseDest {
     return (char*)out[part] + (((size_t)t.b * (part == 0 ? H : Hkv)) * N + t.n) * D * size;
   }
   DMA_DEVINL size_t step(int) const { return (size_t)N * D; }
-  DMA_DEVINL void finish() const {}
 };
 
 template <typename T> constexpr int bwd_rows() { return sizeof(T) == 2 ? 2 : 1; }
@@ -55,9 +55,11 @@ prep_bwd_kernel(const __grid_constant__ PrepArgs a, int wt) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grp = lane / L, e = (lane % L) * 8;
   const bool upper = e >= a.rot >> 1;
   pdl_trigger();
-  for (int k = tid; k < a.rot >> 1; k += kRwThreads) rate[k] = turn_rate(__ldg(a.inv_freq + k));
-  if (lane < kTabPad) tab[warp][D / 2 + lane] = make_float2(1.f, 0.f);
-  __syncthreads();
+  auto ready = [&]() {
+    for (int k = tid; k < a.rot >> 1; k += kRwThreads) rate[k] = turn_rate(__ldg(a.inv_freq + k));
+    if (lane < kTabPad) tab[warp][D / 2 + lane] = make_float2(1.f, 0.f);
+    __syncthreads();
+  };
   auto send = [&](const Walk& at, unsigned char* place) {
     const int part = at.part(), h = at.within(part) * (RPW * U) + grp, heads = part == 0 ? a.H : a.Hkv, left = heads - h;
     const size_t dense = (((size_t)at.b * heads + h) * at.N + at.n) * D + e, step = (size_t)RPW * at.N * D;
@@ -143,7 +145,7 @@ prep_bwd_kernel(const __grid_constant__ PrepArgs a, int wt) {
       dst += RPW * sh;
     }
   };
-  Ring::run(Walk(a, RPW * U, wt), ring_smem, send, work);
+  Ring::run(Walk(a, RPW * U, wt), ring_smem, send, ready, work);
   // the block's partial sums of dg, one row of the workspace each, in the ring's place
   float* red = reinterpret_cast<float*>(ring_smem);   // [kRwWarps * RPW][D]
   static_assert(Ring::kBytes >= kRwWarps * RPW * D * 4, "the sums fit into the ring");
@@ -197,7 +199,7 @@ cudaError_t launch_fwd(const PrepArgs& a, cudaStream_t s) {
   d.positions = a.positions;
   d.N = (unsigned)a.N;
   d.H = a.H; d.Hkv = a.Hkv; d.D = D; d.size = (int)sizeof(T); d.first = a.first;
-  return launch_row_walk<T, D>(a, d, false, s);
+  return launch_row_walk<T, D>(a, d, s);
 }
 
 template <typename T, int D>

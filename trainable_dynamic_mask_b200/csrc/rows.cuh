@@ -224,8 +224,10 @@ template <int NP, int U, int DEPTH> struct RowRing {
       reinterpret_cast<uint4*>(&r)[i] = *reinterpret_cast<const uint4*>(row + (piece + i) * kRwThreads * 16);
     return r;
   }
-  // send(at, place) for every chunk of a walk, DEPTH - 1 chunks ahead of work(at, place)
-  template <typename Send, typename Work> static DMA_DEVINL void run(Walk w, unsigned char* smem, Send send, Work work) {
+  // send(at, place) for every chunk of a walk, DEPTH - 1 chunks ahead of work(at, place); ready() (by every
+  // warp of the block) once the first are on their way
+  template <typename Send, typename Ready, typename Work>
+  static DMA_DEVINL void run(Walk w, unsigned char* smem, Send send, Ready ready, Work work) {
     unsigned char* const ring = smem + threadIdx.x * 16;
     Walk s = w;
     int to = 0, from = 0;
@@ -239,6 +241,7 @@ template <int NP, int U, int DEPTH> struct RowRing {
     };
 #pragma unroll
     for (int i = 0; i < DEPTH - 1; ++i) ahead();
+    ready();
 #pragma unroll 1
     while (w.more()) {
       ahead();
@@ -268,25 +271,29 @@ DMA_DEVINL void token_table(const uint64_t* rate, int half, int position, float2
 }
 
 template <typename T> constexpr int fwd_rows() { return sizeof(T) == 2 ? 4 : 2; }
-template <typename T> using FwdRing = RowRing<sizeof(T) / 2, fwd_rows<T>(), 4>;
+template <typename T, int DEPTH> using FwdRing = RowRing<sizeof(T) / 2, fwd_rows<T>(), DEPTH>;
 
 // Queries and keys normed and rotated, values copied, from the projections (a.in, a.stride) to where Dest
 // says: dest.enter(at, token) (every lane of the warp) is false if nothing of the token is written,
 // else token.position is its position and dest.row(part, token) the address of its first head's row, heads
-// dest.step(part) elements apart.
+// dest.step(part) elements apart.  Dest::kDepth chunks are in flight, Dest::kPerSm
+// CTAs on an SM.
 template <typename T, int D, bool INTER, typename Dest>
 __global__ void __launch_bounds__(kRwThreads, 3)
 row_walk_kernel(const __grid_constant__ PrepArgs a, const __grid_constant__ Dest dest, int wt) {
   constexpr int L = D / 8, RPW = 32 / L, U = fwd_rows<T>();
-  using Ring = FwdRing<T>;
+  using Ring = FwdRing<T, Dest::kDepth>;
   extern __shared__ __align__(128) unsigned char ring_smem[];
   __shared__ __align__(16) float2 tab[kRwWarps][D / 2 + kTabPad];
   __shared__ uint64_t rate[D / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = lane / L, e = (lane % L) * 8;
   const bool upper = e >= a.rot >> 1;
-  for (int k = threadIdx.x; k < a.rot >> 1; k += kRwThreads) rate[k] = turn_rate(__ldg(a.inv_freq + k));
-  if (lane < kTabPad) tab[warp][D / 2 + lane] = make_float2(1.f, 0.f);
-  __syncthreads();
+  pdl_trigger();
+  auto ready = [&]() {
+    for (int k = threadIdx.x; k < a.rot >> 1; k += kRwThreads) rate[k] = turn_rate(__ldg(a.inv_freq + k));
+    if (lane < kTabPad) tab[warp][D / 2 + lane] = make_float2(1.f, 0.f);
+    __syncthreads();
+  };
   auto send = [&](const Walk& at, unsigned char* place) {
     const int part = at.part(), h = at.within(part) * (RPW * U) + grp, left = (part == 0 ? a.H : a.Hkv) - h;
     const long long sh = a.stride[part][2];
@@ -340,19 +347,17 @@ row_walk_kernel(const __grid_constant__ PrepArgs a, const __grid_constant__ Dest
       dst += RPW * sh;
     }
   };
-  Ring::run(Walk(a, RPW * U, wt), ring_smem, send, work);
-  dest.finish();
+  Ring::run(Walk(a, RPW * U, wt), ring_smem, send, ready, work);
 }
 
 template <typename T, int D, typename Dest>
-cudaError_t launch_row_walk(const PrepArgs& a, const Dest& dest, bool dependent, cudaStream_t s) {
+cudaError_t launch_row_walk(const PrepArgs& a, const Dest& dest, cudaStream_t s) {
   int wt;
-  const int blocks = walk_blocks((long long)a.B * a.N, 3, &wt);
+  const int blocks = walk_blocks((long long)a.B * a.N, Dest::kPerSm, &wt);
   auto kernel = a.inter ? row_walk_kernel<T, D, true, Dest> : row_walk_kernel<T, D, false, Dest>;
-  const cudaError_t e = ensure_smem_limit(kernel, FwdRing<T>::kBytes);
+  const cudaError_t e = ensure_smem_limit(kernel, FwdRing<T, Dest::kDepth>::kBytes);
   if (e != cudaSuccess) return e;
-  if (dependent) return launch_after(kernel, dim3(blocks), kRwThreads, FwdRing<T>::kBytes, s, 1, a, dest, wt);
-  kernel<<<blocks, kRwThreads, FwdRing<T>::kBytes, s>>>(a, dest, wt);
+  kernel<<<blocks, kRwThreads, FwdRing<T, Dest::kDepth>::kBytes, s>>>(a, dest, wt);
   return cudaGetLastError();
 }
 
