@@ -38,9 +38,9 @@ struct DenseDest {
   DMA_DEVINL size_t step(int) const { return (size_t)N * D; }
 };
 
-template <typename T> constexpr int bwd_rows() { return sizeof(T) == 2 ? 2 : 1; }
+template <typename T> constexpr int bwd_rows() { return sizeof(T) == 2 ? 4 : 2; }
 // a row's gradient, and its input or (values) the gate's share
-template <typename T> using BwdRing = RowRing<sizeof(T) == 2 ? 3 : 4, bwd_rows<T>(), 4>;
+template <typename T> using BwdRing = RowRing<sizeof(T) == 2 ? 3 : 4, bwd_rows<T>(), 2>;
 
 // Warps walk over the tokens in a fixed order, so the partial sums of the weights' gradients (float32
 // within a lane, at most a few thousand rows each) do not depend on scheduling.
