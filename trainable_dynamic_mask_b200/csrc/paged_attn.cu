@@ -14,6 +14,8 @@
 // candidate's delta with the edge of its row.
 // The partial results (m, l, o) of a row are joined, in a fixed order, by the CTA of its list that
 // finishes last.
+#include <utility>
+
 #include "rows.cuh"
 
 namespace dma {
@@ -248,6 +250,23 @@ constexpr int kPcMost = 256;   // candidates of a CTA at most
 
 template <int D> constexpr int cand_smem() { return (64 + 4 * kPcTile) * D * 2; }   // Q, 2 x (K, V)
 
+// ldmatrix (and its transposing form) at a constant offset from a lane's address.
+template <int OFF> DMA_DEVINL void ldm4(uint32_t at, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4 + %5];\n"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(at), "n"(OFF));
+}
+template <int OFF> DMA_DEVINL void ldm4t(uint32_t at, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4 + %5];\n"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(at), "n"(OFF));
+}
+// f(0) .. f(N - 1), each with its number as a constant
+template <int... I, typename F> DMA_DEVINL void each_of(std::integer_sequence<int, I...>, F f) {
+  (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, typename F> DMA_DEVINL void each(F f) { each_of(std::make_integer_sequence<int, N>(), f); }
+
 // CTA = (part of a head's candidates, head, 16 R sequences).  Its warps (eight, four for R = 1) are R groups
 // of 16 sequences times 2 or 4 groups of keys: with four warps of a group to a tile, a warp's products and
 // exponentials are what a tile takes.  Tiles of 64 candidates' K and V rows
@@ -310,20 +329,32 @@ paged_cand_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ K
   };
   if (nt > 0) load_tile(0);
   cp_async_commit();
-  // this lane's two sequences, s0 + 16 rg + lane / 4 and 8 behind it: their edges
-  uint32_t edge[2];
+  // this lane's two sequences, s0 + 16 rg + lane / 4 and 8 behind it: keys above floor are selected, and where
+  // ties are only partly in (some), those equal to edge among the first cut candidates
+  uint32_t edge[2], floor[2];
   int cut[2];
+  bool some = false;
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     const int s = s0 + rg * 16 + (lane >> 2) + r * 8;
-    edge[r] = 0xffffffffu;
+    edge[r] = floor[r] = 0xffffffffu;
     cut[r] = 0;
     if (s < B) {
       const int4 rec = rows[(size_t)s * H + h];
-      edge[r] = (uint32_t)rec.y;
+      edge[r] = floor[r] = (uint32_t)rec.y;
       cut[r] = rec.z;
+      if (rec.z == 0x7fffffff) floor[r] = edge[r] == 0u ? 0u : edge[r] - 1u;
+      else some = some || rec.z > 0;
     }
   }
+  some = __any_sync(0xffffffffu, some);
+  // addresses of ldmatrix: row and swizzle of a lane do not change from step to step, chunk 2 k of a row being
+  // an exclusive or away from chunk 0
+  const uint32_t qa = smem_u32(Qs) + (rg * 16 + (lane & 15)) * (CH * 16), qx = ((lane >> 4) ^ (lane & 7)) * 16;
+  const int key0 = kg * (kPcTile / KG);   // this warp's keys of a tile
+  const uint32_t ka = smem_u32(Ks) + (key0 + (lane & 7) + (lane >> 4) * 8) * (CH * 16);
+  const uint32_t kx = (((lane >> 3) & 1) ^ (lane & 7)) * 16;
+  const uint32_t va = smem_u32(Vs) + (key0 + (lane & 15)) * (CH * 16);
   float o[NO][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
   for (int n = 0; n < NO; ++n)
@@ -334,7 +365,7 @@ paged_cand_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ K
     cp_async_commit();
     cp_async_wait<1>();
     __syncthreads();
-    const uint32_t kb = smem_u32(Ks + (t & 1) * kPcTile * D), vb = smem_u32(Vs + (t & 1) * kPcTile * D);
+    const uint32_t kb = ka + (t & 1) * kPcTile * D * 2, vb = va + (t & 1) * kPcTile * D * 2;
     // an exponent of all ones anywhere in the V tile
     uint32_t odd = 0u;
     {
@@ -347,24 +378,21 @@ paged_cand_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ K
       }
     }
     const bool plain = __syncthreads_or((odd & 0x80008000u) != 0u);
-    const int key0 = kg * (kPcTile / KG);   // this warp's keys of the tile
     float x[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[n][i] = 0.f;
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
+    each<D / 16>([&](auto k) {
       uint32_t qf[4];
-      ldmatrix_x4(smem_u32(Qs) + swz(rg * 16 + (lane & 15), 2 * k + (lane >> 4), CH), qf[0], qf[1], qf[2], qf[3]);
-#pragma unroll
-      for (int n = 0; n < NT; n += 2) {
+      ldm4<0>(qa + (qx ^ (k * 32)), qf[0], qf[1], qf[2], qf[3]);
+      each<NT / 2>([&](auto n) {
         uint32_t b0, b1, b2, b3;
-        ldmatrix_x4(kb + swz(key0 + n * 8 + (lane & 7) + (lane >> 4) * 8, 2 * k + ((lane >> 3) & 1), CH), b0, b1, b2, b3);
-        mma_bf16_16816(x[n], qf, b0, b1);
-        mma_bf16_16816(x[n + 1], qf, b2, b3);
-      }
-    }
+        ldm4<n * 16 * CH * 16>(kb + (kx ^ (k * 32)), b0, b1, b2, b3);
+        mma_bf16_16816(x[2 * n], qf, b0, b1);
+        mma_bf16_16816(x[2 * n + 1], qf, b2, b3);
+      });
+    });
     float mx[2] = {m[0], m[1]};
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -375,21 +403,36 @@ paged_cand_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ K
       for (int i = 0; i < 4; ++i) {
         const int r = i >> 1;
         const uint32_t k = (i & 1) ? key.y : key.x;
-        const bool take = k > edge[r] || (k == edge[r] && k != 0u && c0 + j + (i & 1) < cut[r]);
+        bool take = k > floor[r];
+        if (some) take = take || (k == edge[r] && k != 0u && c0 + j + (i & 1) < cut[r]);
         x[n][i] = take ? fmaf(x[n][i], scale, (i & 1) ? dl.y : dl.x) : -INFINITY;
         mx[r] = fmaxf(mx[r], x[n][i]);
       }
     }
-    float ref[2], keep[2];
+    // the weights' reference m moves only where a score is far above it: weights up to e^8 are as good
+    float ref[2];
+    bool far = false;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
       mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-      ref[r] = mx[r] == -INFINITY ? 0.f : mx[r];
-      keep[r] = exp_diff(m[r], ref[r]);
-      m[r] = mx[r];
-      l[r] *= keep[r];
+      far = far || mx[r] > m[r] + 8.f;
     }
+    if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float keep = exp_diff(m[r], mx[r] == -INFINITY ? 0.f : mx[r]);
+        m[r] = mx[r];
+        l[r] *= keep;
+#pragma unroll
+        for (int n = 0; n < NO; ++n) {
+          o[n][2 * r] *= keep;
+          o[n][2 * r + 1] *= keep;
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) ref[r] = m[r] == -INFINITY ? 0.f : m[r];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -397,13 +440,8 @@ paged_cand_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ K
         x[n][i] = exp_diff(x[n][i], ref[i >> 1]);
         l[i >> 1] += x[n][i];
       }
-#pragma unroll
-    for (int n = 0; n < NO; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[n][i] *= keep[i >> 1];
     if (!plain) {
-#pragma unroll
-      for (int k = 0; k < NT / 2; ++k) {
+      each<NT / 2>([&](auto k) {
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -411,16 +449,15 @@ paged_cand_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ K
           hi[i] = pack_bf16x2(p0, p1);
           lo[i] = pack_bf16x2(p0 - __uint_as_float(hi[i] << 16), p1 - __uint_as_float(hi[i] & 0xffff0000u));
         }
-#pragma unroll
-        for (int n = 0; n < NO; n += 2) {
+        each<NO / 2>([&](auto n) {
           uint32_t b0, b1, b2, b3;
-          ldmatrix_x4_trans(vb + swz(key0 + k * 16 + (lane & 15), n + (lane >> 4), CH), b0, b1, b2, b3);
-          mma_bf16_16816(o[n], hi, b0, b1);
-          mma_bf16_16816(o[n + 1], hi, b2, b3);
-          mma_bf16_16816(o[n], lo, b0, b1);
-          mma_bf16_16816(o[n + 1], lo, b2, b3);
-        }
-      }
+          ldm4t<k * 16 * CH * 16>(vb + (qx ^ (n * 32)), b0, b1, b2, b3);
+          mma_bf16_16816(o[2 * n], hi, b0, b1);
+          mma_bf16_16816(o[2 * n + 1], hi, b2, b3);
+          mma_bf16_16816(o[2 * n], lo, b0, b1);
+          mma_bf16_16816(o[2 * n + 1], lo, b2, b3);
+        });
+      });
     } else {
       const unsigned char* vrow = reinterpret_cast<const unsigned char*>(Vs + (t & 1) * kPcTile * D);
 #pragma unroll

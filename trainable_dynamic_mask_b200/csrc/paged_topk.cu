@@ -146,7 +146,12 @@ DMA_DEVINL bool rest_by_tail(const PagedPlan& P, const int32_t* tab, int h, int 
     lp[at] = pos;
     le[at] = make_int2((pg << P.page_shift) + (pos & (page - 1)), (int)((k & 0x80000000u) ? k ^ 0x80000000u : ~k));
   }
-  if (tid == 0) *rec = make_int4(out_c, tail[out_c].x, tail[out_c].y + 1, W - out_c);
+  if (tid == 0) {
+    // a cut only where the last to give way ties with the first that stays
+    const int2 stays = tail[out_c];
+    const bool tie = out_c > 0 && tail[max(out_c - 1, 0)].x == stays.x;
+    *rec = make_int4(out_c, stays.x, tie ? stays.y + 1 : 0x7fffffff, W - out_c);
+  }
   return true;
 }
 
