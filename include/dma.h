@@ -461,7 +461,7 @@ dma_status_t dma_paged_layout(const dma_params_t* p, const dma_pages_t* c, dma_p
  * Appends tokens to the cache, from their projections: keys normed and rotated (as in dma_prep, r->positions
  * NULL and r->first ignored: the position is the one in the cache), values copied, gate value formed from the
  * values (as in dma_gate), and the same tokens' queries normed and rotated into Q.
- *   T        tokens in q, k, v;  starts: int32 [B + 1] ascending: sequence b appends the tokens starts[b] ..
+ *   T        tokens in q, k, v (0: nothing is done);  starts: int32 [B + 1] ascending: sequence b appends the tokens starts[b] ..
  *            starts[b+1]-1 as its last positions (of lens[b]); tokens behind starts[B] are padding.  NULL:
  *            T == B, one token each.
  *   q, k, v  strided {-, token, head} as st says (H, Hkv, Hkv heads), dtype;  Q [T, H, d] dtype, dense.  q and

@@ -621,3 +621,102 @@ def test_two_streams_and_graphs_that_share_a_workspace():
     torch.cuda.synchronize()
     for x, y in list(zip(want[0], r1)) + list(zip(w2, r2)):
         assert torch.equal(x, y)
+
+
+def test_calls_that_the_binding_refuses():
+    c = Cache([40, 7], 4, 2, 64, 16, "bf16", 8, seed=50)
+    dma, torch = c.dma, c.torch
+    Q, O, L = c.run()
+    for bad in ((Q.float(), O, L), (Q[:1], O, L), (Q, O.float(), L), (Q, O, L[:, :2]), (Q, O.transpose(0, 1), L),
+                (Q.cpu(), O, L)):
+        with pytest.raises(ValueError):
+            dma.paged_attn(c.p, c.c, bad[0], c.ws, bad[1], bad[2])
+    with pytest.raises(ValueError):
+        dma.paged_topk(c.p, c.c, c.ws.cpu())
+    with pytest.raises(dma.DmaError) as e:
+        dma.paged_topk(c.p, c.c, c.ws[:1024])
+    assert e.value.code == 3
+    for name, bad in (("K", c.K.float()), ("K", c.K[:, :1]), ("V", c.V[:-1]), ("delta", c.delta.to(c.t)),
+                      ("table", c.table.long()), ("table", c.table[:1]), ("lens", c.lens.float())):
+        args = dict(K=c.K, V=c.V, delta=c.delta, table=c.table, lens=c.lens)
+        args[name] = bad
+        with pytest.raises(ValueError):
+            dma.make_pages(c.p, **args)
+    a = _append(c, [3, 2], 64, False, True)
+    call = lambda **kw: dma.paged_append(c.p, c.c, a["r"], *[kw.get(n, a[n]) for n in ("q", "k", "v", "Delta", "A", "Q")],
+                                         c.ws, starts=kw.get("starts", a["starts"]))
+    before = [x.clone() for x in (c.K, c.V, c.delta)]
+    for kw in (dict(v=a["v"][:-1]), dict(Delta=a["Delta"].float()), dict(A=a["A"][:2]), dict(Q=a["Q"][:-1]),
+               dict(starts=a["starts"].long()), dict(starts=a["starts"][:-1]), dict(k=a["k"].cpu())):
+        with pytest.raises(ValueError):
+            call(**kw)
+    with pytest.raises(dma.DmaError):
+        call(starts=None)                        # eight tokens are not one for each of two sequences
+    empty = [a[n][:0] for n in ("q", "k", "v")]
+    dma.paged_append(c.p, c.c, a["r"], *empty, a["Delta"], a["A"], a["Q"][:0], c.ws,
+                     starts=torch.zeros(3, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    for x, y in zip((c.K, c.V, c.delta), before):
+        assert torch.equal(x, y)
+
+
+def test_tables_may_name_the_same_page_twice():
+    """Two sequences over the same pages, and one page at two places of a sequence: reading does not care."""
+    c = Cache([48, 48, 70], 2, 1, 64, 16, "bf16", 20, seed=51)
+    c.table[1] = c.table[0]
+    c.table[2, 3] = c.table[2, 1]
+    Q = c.normal(3, 2, 64).to(c.t)
+    Q[1] = Q[0]
+    out = c.run(Q)
+    c.torch.cuda.synchronize()
+    c.check_selection()
+    c.check(*out)
+    assert c.torch.equal(out[1][0], out[1][1]) and c.torch.equal(out[2][0], out[2][1])
+
+
+def test_rows_far_into_a_large_cache():
+    """Slots whose byte offset passes 32 bits (cache of 4.3 GB): the last pages, at both ends of a table row."""
+    torch = torch_cuda()
+    dma = lib()
+    H, Hkv, d, page, n_pages = 2, 1, 128, 64, 262144 + 8
+    K = torch.zeros((n_pages, Hkv, page, d), dtype=torch.bfloat16, device="cuda")
+    V = torch.zeros_like(K)
+    delta = torch.zeros((n_pages, H, page), device="cuda")
+    lens = torch.tensor([150, 64], dtype=torch.int32, device="cuda")
+    table = torch.tensor([[n_pages - 1, 0, n_pages - 2], [n_pages - 3, -9, -9]], dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    p = dma.make_params(2, H, Hkv, 192, d, 100, Nq=1)
+    pages = dma.make_pages(p, K, V, delta, table, lens)
+    ws = dma.alloc_paged_workspace(p, pages)
+    qkv = torch.randn((214, H + 2 * Hkv, d), generator=g, device="cuda").to(K.dtype)
+    Delta = (0.05 * torch.randn((Hkv * d, H), generator=g, device="cuda")).to(K.dtype)
+    A = -torch.rand(H, generator=g, device="cuda")
+    starts = torch.tensor([0, 150, 214], dtype=torch.int32, device="cuda")
+    Qo = torch.empty((214, H, d), dtype=K.dtype, device="cuda")
+    r = dma.make_prep(None)
+    dma.paged_append(p, pages, r, qkv[:, :H], qkv[:, H:H + 1], qkv[:, H + 1:], Delta, A, Qo, ws, starts=starts)
+    assert torch.equal(K[n_pages - 1, 0], qkv[:64, H]) and torch.equal(V[n_pages - 3, 0], qkv[150:, H + 1])
+    assert torch.equal(K[n_pages - 2, 0, :22], qkv[128:150, H]) and (K[1:n_pages - 3] == 0).all()
+    Q = torch.randn((2, H, d), generator=g, device="cuda").to(K.dtype)
+    O, L = torch.empty_like(Q), torch.empty((2, H), device="cuda")
+    dma.paged_topk(p, pages, ws)
+    dma.paged_attn(p, pages, Q, ws, O, L)
+    assert dma.check_device_status(p, ws) == 0
+    # the same rows in a small cache give the same bits
+    small = [x[[0, n_pages - 1, n_pages - 2, n_pages - 3]].contiguous() for x in (K, V, delta)]
+    t2 = torch.tensor([[1, 0, 2], [3, -9, -9]], dtype=torch.int32, device="cuda")
+    pages2 = dma.make_pages(p, *small, t2, lens)
+    O2, L2 = torch.empty_like(O), torch.empty_like(L)
+    dma.paged_topk(p, pages2, ws)
+    dma.paged_attn(p, pages2, Q, ws, O2, L2)
+    assert torch.equal(O, O2) and torch.equal(L, L2)
+
+
+def test_prefix_that_is_everything():
+    """No position behind the prefix, for any sequence or for all that the problem allows."""
+    for N in (96, 128):
+        c = Cache([96, 96, 0, 96], 4, 2, 64, 32, "bf16", 40, seed=52, prefix=96, N=N)
+        out = c.run()
+        c.torch.cuda.synchronize()
+        c.check_selection()
+        c.check(*out)

@@ -270,3 +270,75 @@ def test_other_stream_and_captured_graph():
     for a in (other, got):
         for x, y in zip(sum(want, []), sum(a, [])):
             assert torch.equal(x, y)
+
+
+def test_calls_that_the_binding_refuses():
+    dma = lib()
+    torch, t = _types("bf16")
+    p = dma.make_params(2, 4, 2, 10, 64, 1)
+    q, k = torch.zeros(2, 10, 4, 64, dtype=t, device="cuda"), torch.zeros(2, 10, 2, 64, dtype=t, device="cuda")
+    Q, K = torch.zeros(2, 4, 10, 64, dtype=t, device="cuda"), torch.zeros(2, 2, 10, 64, dtype=t, device="cuda")
+    r = dma.make_prep(_freq(torch, 64))
+    good = dict(q=q, k=k, v=k, Q=Q, K=K, V=torch.zeros_like(K))
+    dma.prep(p, r, *good.values())
+    for name, bad in (("q", q.float()), ("q", q[:, :9]), ("k", k.cpu()), ("Q", Q.transpose(1, 2)),
+                      ("Q", Q.transpose(1, 2).contiguous().transpose(1, 2)), ("K", K[..., :32]),
+                      ("q", torch.zeros(2, 10, 64, 4, dtype=t, device="cuda").transpose(2, 3))):
+        with pytest.raises(ValueError, match=name):
+            dma.prep(p, r, *{**good, name: bad}.values())
+    for kw in (dict(q_weight=torch.zeros(64, device="cuda")), dict(k_weight=torch.zeros(32, dtype=t, device="cuda")),
+               dict(positions=torch.zeros(2, 10, device="cuda")),
+               dict(positions=torch.zeros(2, 9, dtype=torch.int32, device="cuda"))):
+        with pytest.raises(ValueError):
+            dma.prep(p, dma.make_prep(_freq(torch, 64), **kw), *good.values())
+    with pytest.raises(ValueError):
+        dma.prep(p, dma.make_prep(_freq(torch, 64).cpu()), *good.values())
+    odd = torch.zeros(2 * 10 * 4 * 64 + 4, dtype=t, device="cuda")[4:].view(2, 10, 4, 64)   # 8 bytes off
+    with pytest.raises(dma.DmaError) as e:
+        dma.prep(p, r, odd, *list(good.values())[1:])
+    assert e.value.code == 1
+
+
+def test_training_step_from_projections_and_back():
+    """Projections -> prep -> gate -> selection -> attention, and the gradients all the way back to the
+    projections.  Each stage is held to its own tolerance on the inputs the GPU gave it; the last (prep_bwd) to the
+    whole: the attention's 2e-2 + 1e-2 |x| on its gradients, carried through the rows' Jacobian in magnitudes."""
+    import oracle
+    from gpu_common import assert_close
+    dma = lib()
+    B, N, H, Hkv, d, w = 1, 200, 4, 2, 64, 48
+    c = _case(B, N, H, Hkv, d, "bf16", 64, False, True, True, seed=12)
+    torch, t = c["torch"], c["t"]
+    p = dma.make_params(B, H, Hkv, N, d, w)
+    r = dma.make_prep(c["freq"], c["qw"], c["kw"], eps=1e-5)
+    Q, K, V = (torch.empty((B, h, N, d), dtype=t, device="cuda") for h in (H, Hkv, Hkv))
+    Delta, A = (0.05 * c["normal"](Hkv * d, H)).to(t), -torch.rand(H, device="cuda")
+    dma.prep(p, r, c["q"], c["k"], c["v"], Q, K, V)
+    fwd = dma.forward(p, Q, K, V, Delta, A)
+    dO = c["normal"](B, H, N, d).to(t)
+    bwd = dma.backward(p, Q, K, V, Delta, A, fwd, dO)
+    grad = torch.empty(B, N, H + 2 * Hkv, d, dtype=t, device="cuda")
+    gq, gk, gv = grad[:, :, :H], grad[:, :, H:H + Hkv], grad[:, :, H + Hkv:]
+    dqw, dkw = torch.empty(d, device="cuda"), torch.empty(d, device="cuda")
+    dma.prep_bwd(p, r, c["q"], c["k"], bwd["dQ"], bwd["dK"], bwd["dV"], bwd["dV_gate"], gq, gk, gv, dqw, dkw,
+                 dma.alloc_prep_workspace(p, r))
+    torch.cuda.synchronize()
+    # the oracle on the inputs that prep made
+    delta = fwd["delta"].cpu().numpy()
+    evict = np.stack([oracle.topw_eviction(delta[0, h], w) for h in range(H)])[None]
+    Qn, Kn, Vn = _np(Q), _np(K), _np(V)
+    O, _ = oracle.attn_fwd(Qn, Kn, Vn, delta.astype(np.float64), evict)
+    assert_close(fwd["O"].float().cpu().numpy(), O, "O")
+    rQ, rK, rV, rd = oracle.attn_bwd(Qn, Kn, Vn, delta.astype(np.float64), evict, _np(dO))
+    _, _, rVg = oracle.gate_bwd(Vn, _np(Delta), _np(A), bwd["d_delta"].cpu().numpy().astype(np.float64))
+    R = _R(c, B, N, d)
+    eps = np.float64(np.float32(1e-5))
+    for got, gw, x, wt, dy in ((gq, dqw, c["q"], c["qw"], rQ), (gk, dkw, c["k"], c["kw"], rK)):
+        x, wt, dy = _np(x), _np(wt), dy.transpose(0, 2, 1, 3)
+        ref, mag, rw, mw = _backward(x, wt, R, eps, dy)
+        _, slack, _, slack_w = _backward(x, wt, R, eps, 2e-2 + 1e-2 * np.abs(dy))
+        assert (np.abs(_np(got) - ref) <= slack + 2.0 ** -8 * (np.abs(ref) + slack) + 40 * U * mag).all()
+        assert (np.abs(_np(gw) - rw) <= slack_w + (40 + 2 * N) * U * mw).all()
+    ref = rV.transpose(0, 2, 1, 3) + rVg.transpose(0, 2, 1, 3)
+    tol = 2e-2 + 1e-2 * np.abs(rV.transpose(0, 2, 1, 3)) + 2e-2 + 1e-2 * np.abs(rVg.transpose(0, 2, 1, 3))
+    assert (np.abs(_np(gv) - ref) <= tol + 2.0 ** -8 * (np.abs(ref) + tol)).all()

@@ -236,12 +236,9 @@ def make_prep(inv_freq, q_weight=None, k_weight=None, eps=1e-6, positions=None, 
     norm.  positions: device int32 [B, N]; None: first, first + 1, ...  interleaved: the
     pairs are neighbouring channels instead of the two halves.  The result keeps the
     tensors alive."""
-    import torch
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    r = DmaPrep(inv_freq=_dense("inv_freq", inv_freq, (rot // 2,), torch.float32, dev), eps=float(eps), rot=rot,
+    r = DmaPrep(inv_freq=_ptr(inv_freq), positions=_ptr(positions), q_weight=_ptr(q_weight), k_weight=_ptr(k_weight),
+                eps=float(eps), rot=0 if inv_freq is None else 2 * inv_freq.numel(),
                 interleaved=1 if interleaved else 0, first=int(first))
-    r.q_weight, r.k_weight, r.positions = _ptr(q_weight), _ptr(k_weight), _ptr(positions)
     r.tensors = (inv_freq, q_weight, k_weight, positions)
     r.fits = None
     return r
@@ -249,10 +246,11 @@ def make_prep(inv_freq, q_weight=None, k_weight=None, eps=1e-6, positions=None, 
 
 def _check_prep_tensors(p, r, dev):
     """The weights and positions of r fit p (looked at again when p's sizes change)."""
-    import torch
     key = (p.B, p.N, p.d, p.dtype, dev)
     if r.fits != key:
-        _, qw, kw, pos = r.tensors
+        import torch
+        freq, qw, kw, pos = r.tensors
+        _dense("inv_freq", freq, (r.rot // 2,), torch.float32, dev)
         _dense("q_weight", qw, (p.d,), _storage(p), dev)
         _dense("k_weight", kw, (p.d,), _storage(p), dev)
         _dense("positions", pos, (p.B, p.N), torch.int32, dev)
@@ -264,11 +262,12 @@ def prep(p, r, q, k, v, Q, K, V, stream=None):
     Q [B, H, N, d], K, V [B, Hkv, N, d]: per-head norm, rotation and transposition in one pass.
     v and V may be None together."""
     import torch
+    call = load().dma_prep
     dev, t = torch.cuda.current_device(), _storage(p)
     B, H, Hkv, N, d = p.B, p.H, p.Hkv, p.N, p.d
     _check_prep_tensors(p, r, dev)
     st = DmaPrepStrides()
-    check("dma_prep", load().dma_prep(
+    check("dma_prep", call(
         p, r, st, _rows("q", q, (B, N, H, d), t, dev, st.q), _rows("k", k, (B, N, Hkv, d), t, dev, st.k),
         _rows("v", v, (B, N, Hkv, d), t, dev, st.v), _dense("Q", Q, (B, H, N, d), t, dev),
         _dense("K", K, (B, Hkv, N, d), t, dev), _dense("V", V, (B, Hkv, N, d), t, dev), _stream_on(stream, dev)))
@@ -285,12 +284,13 @@ def prep_bwd(p, r, q, k, dQ, dK, dV, dV_gate, dq, dk, dv, dq_weight, dk_weight, 
     strides ([B, N, heads, d]), dV_gate (float32, or None) is added to dV, dq_weight and dk_weight are
     float32 [d] (None: not wanted); q, k as in prep (None where there is no weight)."""
     import torch
+    call = load().dma_prep_bwd
     dev, t, f = torch.cuda.current_device(), _storage(p), torch.float32
     B, H, Hkv, N, d = p.B, p.H, p.Hkv, p.N, p.d
     _check_prep_tensors(p, r, dev)
     st, gst = DmaPrepStrides(), DmaPrepStrides()
     sq, sk, hq, hk = (B, N, H, d), (B, N, Hkv, d), (B, H, N, d), (B, Hkv, N, d)
-    check("dma_prep_bwd", load().dma_prep_bwd(
+    check("dma_prep_bwd", call(
         p, r, st, gst, _rows("q", q, sq, t, dev, st.q), _rows("k", k, sk, t, dev, st.k), _dense("dQ", dQ, hq, t, dev),
         _dense("dK", dK, hk, t, dev), _dense("dV", dV, hk, t, dev), _dense("dV_gate", dV_gate, hk, f, dev),
         _rows("dq", dq, sq, t, dev, gst.q), _rows("dk", dk, sk, t, dev, gst.k), _rows("dv", dv, sk, t, dev, gst.v),
@@ -322,8 +322,13 @@ def make_pages(p, K, V, delta, table, lens, prefix=0) -> DmaPages:
                  table=_dense("table", table, (p.B, table.shape[1]), torch.int32, dev),
                  lens=_dense("lens", lens, (p.B,), torch.int32, dev), n_pages=n, page=page,
                  max_pages=table.shape[1], prefix=int(prefix))
-    c.tensors = (K, V, delta, table, lens)
+    c.tensors, c.device = (K, V, delta, table, lens), dev
     return c
+
+
+def _same_device(c, dev):
+    if c.device != dev:
+        raise ValueError(f"the pages are on cuda:{c.device}, the current device is cuda:{dev}")
 
 
 def paged_layout(p, c) -> DmaPagedLayout:
@@ -338,11 +343,13 @@ def paged_append(p, c, r, q, k, v, Delta, A, Q, workspace, starts=None, stream=N
     normed and rotated queries (q and Q may be None together).  starts: device int32 [B + 1], the
     sequences' token ranges; None: one token each."""
     import torch
+    call = load().dma_paged_append
     dev, t, f = torch.cuda.current_device(), _storage(p), torch.float32
     T, H, Hkv, d = k.shape[0], p.H, p.Hkv, p.d
+    _same_device(c, dev)
     _check_prep_tensors(p, r, dev)
     st = DmaPrepStrides()
-    check("dma_paged_append", load().dma_paged_append(
+    check("dma_paged_append", call(
         p, c, r, st, T, _dense("starts", starts, (p.B + 1,), torch.int32, dev),
         _rows("q", q, (T, H, d), t, dev, st.q), _rows("k", k, (T, Hkv, d), t, dev, st.k),
         _rows("v", v, (T, Hkv, d), t, dev, st.v), _dense("Delta", Delta, (Hkv * d, H), t, dev),
@@ -353,17 +360,21 @@ def paged_append(p, c, r, q, k, v, Delta, A, Q, workspace, starts=None, stream=N
 def paged_topk(p, c, workspace, stream=None):
     """Selection of every (sequence, head) over its cache, into the workspace."""
     import torch
+    call = load().dma_paged_topk
     dev = torch.cuda.current_device()
-    check("dma_paged_topk", load().dma_paged_topk(p, c, _workspace(workspace, dev), _nbytes(workspace),
+    _same_device(c, dev)
+    check("dma_paged_topk", call(p, c, _workspace(workspace, dev), _nbytes(workspace),
                                                   _stream_on(stream, dev)))
 
 
 def paged_attn(p, c, Q, workspace, O, LSE, stream=None):
     """Attention of one query [B, H, d] for each sequence over the keys paged_topk selected."""
     import torch
+    call = load().dma_paged_attn
     dev, t = torch.cuda.current_device(), _storage(p)
     shape = (p.B, p.H, p.d)
-    check("dma_paged_attn", load().dma_paged_attn(
+    _same_device(c, dev)
+    check("dma_paged_attn", call(
         p, c, _dense("Q", Q, shape, t, dev), _workspace(workspace, dev), _nbytes(workspace),
         _dense("O", O, shape, t, dev), _dense("LSE", LSE, (p.B, p.H), torch.float32, dev), _stream_on(stream, dev)))
 

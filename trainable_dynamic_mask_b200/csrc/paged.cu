@@ -16,6 +16,7 @@ dma_status_t paged_plan(const dma_params_t* p, const dma_pages_t* c, PagedPlan* 
   if (!ok_ptr(c->K) || !ok_ptr(c->V) || !ok_ptr(c->delta) || !ok_ptr(c->table) || !ok_ptr(c->lens))
     return DMA_ERR_INVALID_ARG;
   if (c->n_pages < 1 || c->max_pages < 1 || c->page < 1 || c->prefix < 0) return DMA_ERR_INVALID_ARG;
+  if ((p->w < p->N ? p->w : p->N) > 4096 * p->d) return DMA_ERR_UNSUPPORTED;
   if (c->page < 16 || c->page > 1024 || (c->page & (c->page - 1)) != 0) return DMA_ERR_UNSUPPORTED;
   if ((int64_t)c->n_pages * c->page >= ((int64_t)1 << 31) || (int64_t)c->n_pages * p->H >= ((int64_t)1 << 31)) return DMA_ERR_UNSUPPORTED;
   if (p->N > (int64_t)c->max_pages * c->page || c->prefix % c->page != 0 || c->prefix > p->N)
@@ -104,14 +105,14 @@ dma_status_t dma_paged_append(const dma_params_t* p, const dma_pages_t* c, const
   if ((st = check_prep(r, P.d)) != DMA_OK) return st;
   if (r->positions != nullptr || strides == nullptr || T < 0) return DMA_ERR_INVALID_ARG;
   if (starts == nullptr ? T != P.B : !ok_ptr(starts)) return DMA_ERR_INVALID_ARG;
+  if (P.H > kGateMaxH) return DMA_ERR_UNSUPPORTED;
+  if ((st = check_ws(P, workspace, workspace_bytes)) != DMA_OK) return st;
+  if (T == 0) return DMA_OK;   // no token, no tensors
   if ((q == nullptr) != (Q == nullptr) || (q != nullptr && (!ok_ptr(q) || !ok_ptr(Q)))) return DMA_ERR_INVALID_ARG;
   if (!ok_ptr(k) || !ok_ptr(v) || !ok_ptr(Delta) || !ok_ptr(A)) return DMA_ERR_INVALID_ARG;
   if ((q != nullptr && !check_strides(strides->q, P.bf16)) || !check_strides(strides->k, P.bf16) ||
       !check_strides(strides->v, P.bf16))
     return DMA_ERR_INVALID_ARG;
-  if (P.H > kGateMaxH) return DMA_ERR_UNSUPPORTED;
-  if ((st = check_ws(P, workspace, workspace_bytes)) != DMA_OK) return st;
-  if (T == 0) return DMA_OK;
   PagedAppendArgs a;
   a.r = *r;
   a.st = *strides;
