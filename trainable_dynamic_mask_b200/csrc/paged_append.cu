@@ -2,11 +2,10 @@
 // values delta = exp(A softplus(v Delta)) formed from the values on the way, queries of the same tokens
 // normed and rotated.
 //
-// Two kernels that run side by side: the walk over the rows (rows.cuh, as in prep.cu) and the gate's product
-// (the values of 16 tokens against Delta, tensor cores for bf16).  The second is launched as a
-// programmatic dependent of the first, which lets it go at once; it waits for the first only before it
-// ends, so that whatever follows in the stream finds both done.  The rows' shares of the work are fixed when
-// they start and theirs is the longer way, so they come first.
+// One kernel, two kinds of CTAs side by side: the first walk over the rows (rows.cuh, as in prep.cu), the
+// others form the gate's product (the values of 16 tokens against Delta, tensor cores for bf16).  The walk's
+// shares are fixed when it starts and it is the longer way, so it comes first, with two CTAs an SM; the
+// gate's CTAs follow one another in the place that is left.
 #include "rows.cuh"
 
 namespace dma {
@@ -53,7 +52,7 @@ DMA_DEVINL Place place_of(const PagedPlan& P, const PagedAppendArgs& a, int t, i
 // Keys and values to their slots, queries to Q [T, H, D].  A warp looks up the places of its next 32 tokens
 // together, a token a lane: the lookups' three or more dependent reads are then paid once.
 struct SlotDest {
-  static constexpr int kDepth = 4, kPerSm = 2;   // two CTAs an SM leave the registers for the gate
+  static constexpr int kDepth = 4;
   struct Token {
     int position;
     unsigned tok;
@@ -92,7 +91,7 @@ struct SlotDest {
 // ---------------------------------------------------------------- gate, tensor cores
 
 constexpr int kAgTok = 16;        // tokens of a CTA: one m16 tile
-constexpr int kAgThreads = 256;
+constexpr int kAgThreads = kRwThreads;
 constexpr int kAgWarps = kAgThreads / 32;
 
 // Offset of (token's page, head 0, slot) in the delta pages of the CTA's tokens; -1: none.
@@ -118,9 +117,7 @@ template <int HT> constexpr int gate_smem() {
 // in float32, in which all is accumulated.  Two stages (32 to 80 KB) rather than all of K at once leave
 // room for the rows' CTAs beside these.
 template <int HT>   // column tiles of 8 heads
-__global__ void __launch_bounds__(kAgThreads)
-paged_gate_mma_kernel(const __grid_constant__ PagedPlan P, const __grid_constant__ PagedAppendArgs a, int32_t* status) {
-  extern __shared__ __align__(128) unsigned char sm[];
+DMA_DEVINL void gate_mma(const PagedPlan& P, const PagedAppendArgs& a, int32_t* status, int block, unsigned char* sm) {
   __shared__ long long where[kAgTok];
   constexpr int KC = kAgK / 8, kStage = kAgK * (kAgTok + 8 * HT);   // elements
   uint16_t* const stage = reinterpret_cast<uint16_t*>(sm);   // [2]: v [16][256], chunk c of row r at c ^ (r & 7);
@@ -128,7 +125,7 @@ paged_gate_mma_kernel(const __grid_constant__ PagedPlan P, const __grid_constant
   float* red = reinterpret_cast<float*>(sm);                 // [8 warps][16][8 HT], in the stages' place
   const int K = P.Hkv * P.d, dch = P.d / 8, n_st = (K + kAgK - 1) / kAgK;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int t0 = blockIdx.x * kAgTok;
+  const int t0 = block * kAgTok;
   const uint16_t* v = static_cast<const uint16_t*>(a.v);
   const uint16_t* Delta = static_cast<const uint16_t*>(a.Delta);
   auto load = [&](int st) {
@@ -204,7 +201,6 @@ paged_gate_mma_kernel(const __grid_constant__ PagedPlan P, const __grid_constant
     for (int w = 0; w < kAgWarps; ++w) x += red[((size_t)w * kAgTok + t) * 8 * HT + h];
     P.delta[at + ((long long)h << P.page_shift)] = expf(a.A[h] * softplus_of(x));
   }
-  pdl_wait();   // the rows' kernel in front is done too
 }
 
 // ---------------------------------------------------------------- gate, float32
@@ -214,15 +210,13 @@ constexpr int kAfK = 512;      // channels staged at a time
 
 // float32 storage: the same product on the FMA pipe, with the values' full precision.  Thread = one head and
 // one of NS slices of the staged channels, for 8 tokens.
-__global__ void __launch_bounds__(kAgThreads)
-paged_gate_kernel(const __grid_constant__ PagedPlan P, const __grid_constant__ PagedAppendArgs a, int HP, int32_t* status) {
-  extern __shared__ __align__(16) float fsm[];
+DMA_DEVINL void gate_fma(const PagedPlan& P, const PagedAppendArgs& a, int32_t* status, int block, float* fsm) {
   __shared__ long long where[kAfTok];
   float* Vs = fsm;                   // [kAfK][kAfTok]
   float* red = Vs + kAfK * kAfTok;   // [NS][kAfTok][HP]
-  const int K = P.Hkv * P.d, NS = kAgThreads / HP;
+  const int K = P.Hkv * P.d, HP = P.H <= 16 ? 16 : P.H <= 32 ? 32 : 64, NS = kAgThreads / HP;
   const int tid = threadIdx.x, h = tid % HP, sl = tid / HP;
-  const int t0 = blockIdx.x * kAfTok;
+  const int t0 = block * kAfTok;
   const float* v = static_cast<const float*>(a.v);
   const float* Delta = static_cast<const float*>(a.Delta);
   gate_places(P, a, t0, kAfTok, where, status);
@@ -264,30 +258,51 @@ paged_gate_kernel(const __grid_constant__ PagedPlan P, const __grid_constant__ P
     for (int s = 0; s < NS; ++s) x += red[(s * kAfTok + t) * HP + hh];
     P.delta[at + ((long long)hh << P.page_shift)] = expf(a.A[hh] * softplus_of(x));
   }
-  pdl_wait();   // the rows' kernel in front is done too
 }
 
-template <int HT>
-cudaError_t launch_gate_mma(const PagedPlan& P, const PagedAppendArgs& a, int32_t* status, cudaStream_t s) {
-  const cudaError_t e = ensure_smem_limit(paged_gate_mma_kernel<HT>, gate_smem<HT>());
+// ---------------------------------------------------------------- both
+
+template <typename T, int HT> constexpr int append_smem() {
+  constexpr int rows = FwdRing<T, SlotDest::kDepth>::kBytes;
+  constexpr int gate = HT > 0 ? gate_smem<HT>() : (kAfK * kAfTok + kAgThreads * kAfTok) * 4;
+  return rows > gate ? rows : gate;
+}
+
+// HT: column tiles of the gate's product (bf16), or 0 (float32).
+template <typename T, int D, bool INTER, int HT>
+__global__ void __launch_bounds__(kRwThreads, 3)
+paged_append_kernel(const __grid_constant__ PrepArgs w, const __grid_constant__ SlotDest dest, int wt, int row_blocks) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int block = (int)blockIdx.x - row_blocks;
+  if (block < 0) {
+    walk_rows<T, D, INTER>(w, dest, wt, blockIdx.x, row_blocks, smem);
+  } else {
+    if constexpr (HT > 0) gate_mma<HT>(dest.P, dest.a, dest.status, block, smem);
+    else gate_fma(dest.P, dest.a, dest.status, block, reinterpret_cast<float*>(smem));
+  }
+}
+
+template <typename T, int D, int HT>
+cudaError_t launch_append(const PrepArgs& w, const SlotDest& d, cudaStream_t s) {
+  int wt;
+  const int row_blocks = walk_blocks(d.a.T, 2, &wt), tok = HT > 0 ? kAgTok : kAfTok;
+  constexpr int smem = append_smem<T, HT>();
+  auto kernel = w.inter ? paged_append_kernel<T, D, true, HT> : paged_append_kernel<T, D, false, HT>;
+  const cudaError_t e = ensure_smem_limit(kernel, smem);
   if (e != cudaSuccess) return e;
-  return launch_after(paged_gate_mma_kernel<HT>, dim3((a.T + kAgTok - 1) / kAgTok), kAgThreads, gate_smem<HT>(), s, 1, P, a,
-                      status);
+  kernel<<<row_blocks + (d.a.T + tok - 1) / tok, kRwThreads, smem, s>>>(w, d, wt, row_blocks);
+  return cudaGetLastError();
 }
 
-cudaError_t launch_gate(const PagedPlan& P, const PagedAppendArgs& a, int32_t* status, cudaStream_t s) {
-  if (P.bf16)
-    return P.H <= 16   ? launch_gate_mma<2>(P, a, status, s)
-           : P.H <= 32 ? launch_gate_mma<4>(P, a, status, s)
-                       : launch_gate_mma<8>(P, a, status, s);
-  const int HP = P.H <= 16 ? 16 : P.H <= 32 ? 32 : 64;
-  const int smem = (kAfK * kAfTok + kAgThreads * kAfTok) * (int)sizeof(float);
-  const int blocks = (a.T + kAfTok - 1) / kAfTok;
-  return launch_after(paged_gate_kernel, dim3(blocks), kAgThreads, smem, s, 1, P, a, HP, status);
+template <int D> cudaError_t launch_append_bf16(const PrepArgs& w, const SlotDest& d, cudaStream_t s) {
+  if (d.P.H <= 16) return launch_append<uint16_t, D, 2>(w, d, s);
+  if (d.P.H <= 32) return launch_append<uint16_t, D, 4>(w, d, s);
+  return launch_append<uint16_t, D, 8>(w, d, s);
 }
 
-template <typename T, int D>
-cudaError_t launch_rows(const PagedPlan& P, const PagedAppendArgs& a, int32_t* status, cudaStream_t s) {
+}  // namespace
+
+cudaError_t launch_paged_append(const PagedPlan& P, const PagedAppendArgs& a, void* ws, cudaStream_t s) {
   PrepArgs w = {};
   w.inv_freq = a.r.inv_freq;
   w.weight[0] = a.r.q_weight;
@@ -305,21 +320,10 @@ cudaError_t launch_rows(const PagedPlan& P, const PagedAppendArgs& a, int32_t* s
   SlotDest d = {};
   d.P = P;
   d.a = a;
-  d.status = status;
-  d.size = (int)sizeof(T);
-  return launch_row_walk<T, D>(w, d, s);
-}
-
-}  // namespace
-
-cudaError_t launch_paged_append(const PagedPlan& P, const PagedAppendArgs& a, void* ws, cudaStream_t s) {
-  int32_t* status = ws_ptr<int32_t>(ws, P.off_status);
-  cudaError_t e;
-  if (P.bf16)
-    e = P.d == 128 ? launch_rows<uint16_t, 128>(P, a, status, s) : launch_rows<uint16_t, 64>(P, a, status, s);
-  else
-    e = P.d == 128 ? launch_rows<float, 128>(P, a, status, s) : launch_rows<float, 64>(P, a, status, s);
-  return e == cudaSuccess ? launch_gate(P, a, status, s) : e;
+  d.status = ws_ptr<int32_t>(ws, P.off_status);
+  d.size = P.bf16 ? 2 : 4;
+  if (P.bf16) return P.d == 128 ? launch_append_bf16<128>(w, d, s) : launch_append_bf16<64>(w, d, s);
+  return P.d == 128 ? launch_append<float, 128, 0>(w, d, s) : launch_append<float, 64, 0>(w, d, s);
 }
 
 }  // namespace dma

@@ -240,6 +240,8 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
     sh.members = 0;
     msh = sh;
     listed_total = 0;
+    found_bin = found_above = found_count = 0;
+    found_key = 0u;
   }
   *reinterpret_cast<int4*>(hist + 4 * tid) = make_int4(0, 0, 0, 0);
   if (SIEVE) *reinterpret_cast<int4*>(mhist + 4 * tid) = make_int4(0, 0, 0, 0);
@@ -618,12 +620,12 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
       if (found_count <= NT) {
         // rank the interval's keys against each other
         for_keys([&](uint32_t k) {
-          if (k >= lo && k - lo <= span) list[atomicAdd(&sh.members, 1)] = k;
+          if (k >= lo && k - lo <= span) list[min(atomicAdd(&sh.members, 1), NT - 1)] = k;
         });
         all_sync();
         int m = 0;
         for (int r = 0; r < C; ++r) {
-          const int mr = of(&sh, r)->members;
+          const int mr = min(of(&sh, r)->members, NT - m);
           if (tid < mr) every[m + tid] = *of(list + tid, r);
           m += mr;
         }
@@ -692,21 +694,21 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
   } else if (!bad) {
     auto count = [&](auto resident) {
 #pragma unroll 4
-    for (int j = j0 + lane * 4; j < j1; j += 128) {
-      const uint4 k4 = resident || j < cap ? *reinterpret_cast<const uint4*>(keys + j) : load4(i0 + j);
-      const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
-      const bool c = M == kRest && i0 + j < n1p;   // n1p and j are multiples of 4
+      for (int j = j0 + lane * 4; j < j1; j += 128) {
+        const uint4 k4 = resident || j < cap ? *reinterpret_cast<const uint4*>(keys + j) : load4(i0 + j);
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+        const bool c = M == kRest && i0 + j < n1p;   // n1p and j are multiples of 4
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int gt = k[u] > T, eq = k[u] == T && T != 0u;
-        if (M == kRest) {
-          cnt[0] += c ? gt : 0;
-          cnt[1] += c ? eq : 0;
+        for (int u = 0; u < 4; ++u) {
+          const int gt = k[u] > T, eq = k[u] == T && T != 0u;
+          if (M == kRest) {
+            cnt[0] += c ? gt : 0;
+            cnt[1] += c ? eq : 0;
+          }
+          cnt[2] += c ? 0 : gt;
+          cnt[3] += c ? 0 : eq;
         }
-        cnt[2] += c ? 0 : gt;
-        cnt[3] += c ? 0 : eq;
       }
-    }
     };
     if (items <= cap) count(Yes());
     else count(No());
@@ -759,7 +761,8 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
     }
   }
 
-  // ---- the list
+  // ---- the list (room, like the limits above: values that change while they are read must not lead out of it)
+  const int room = M == kCandidates ? P.cand_len : P.sel_len;
   if (SIEVE && sieved) {
     const int gt0 = cta_in.x, eq0 = cta_in.y;
     int32_t* lp = sel + (size_t)row * P.sel_len;
@@ -773,8 +776,9 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
         const unsigned em = __ballot_sync(0xffffffffu, k == T);   // T is a key of the row, not 0
         const bool take = k > T || (k == T && eq + __popc(em & lt) < need);
         const unsigned tm = __ballot_sync(0xffffffffu, take);
-        if (take) {
-          const int at = out + __popc(tm & lt), pos = index[bb.x + j];
+        const int at = out + __popc(tm & lt);
+        if (take && at < room) {
+          const int pos = index[bb.x + j];
           lp[at] = pos;
           le[at] = make_int2(slot_of(pos), (int)((k & 0x80000000u) ? k ^ 0x80000000u : ~k));
         }
@@ -789,56 +793,58 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
     int2* le = M == kCandidates ? cent + (size_t)h * P.cand_len : ent + (size_t)row * P.sel_len;
     const unsigned lt = (1u << lane) - 1u;
     auto emit = [&](auto resident) {
-    for (int j = j0; j < j1; j += 128) {
-      const int jl = j + lane * 4, i = i0 + jl;
-      uint4 k4 = make_uint4(0u, 0u, 0u, 0u);
-      if (jl < j1) k4 = resident || jl < cap ? *reinterpret_cast<const uint4*>(keys + jl) : load4(i0 + jl);
-      const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
-      const bool c = M == kRest && i < n1p;
-      bool take[4];
+      for (int j = j0; j < j1; j += 128) {
+        const int jl = j + lane * 4, i = i0 + jl;
+        uint4 k4 = make_uint4(0u, 0u, 0u, 0u);
+        if (jl < j1) k4 = resident || jl < cap ? *reinterpret_cast<const uint4*>(keys + jl) : load4(i0 + jl);
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+        const bool c = M == kRest && i < n1p;
+        bool take[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) take[u] = k[u] > T && !c;
-      const bool has = T != 0u && (k[0] == T || k[1] == T || k[2] == T || k[3] == T);
-      if (__any_sync(0xffffffffu, has)) {   // ties, in the order of positions
-        int before = eq, sum = 0;
+        for (int u = 0; u < 4; ++u) take[u] = k[u] > T && !c;
+        const bool has = T != 0u && (k[0] == T || k[1] == T || k[2] == T || k[3] == T);
+        if (__any_sync(0xffffffffu, has)) {   // ties, in the order of positions
+          int before = eq, sum = 0;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const unsigned em = __ballot_sync(0xffffffffu, k[u] == T);
-          before += __popc(em & lt);
-          sum += __popc(em);
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (k[u] == T) {
-            if (!c) take[u] = before < need;
-            else if (before == need - 1 && ties_c < all[1]) rec[2] = i + u + 1;
-            ++before;
+          for (int u = 0; u < 4; ++u) {
+            const unsigned em = __ballot_sync(0xffffffffu, k[u] == T);
+            before += __popc(em & lt);
+            sum += __popc(em);
           }
-        eq += sum;
-      }
-      unsigned tm[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) tm[u] = __ballot_sync(0xffffffffu, take[u]);
-      if ((tm[0] | tm[1] | tm[2] | tm[3]) == 0u) continue;
-      int at = out + __popc(tm[0] & lt) + __popc(tm[1] & lt) + __popc(tm[2] & lt) + __popc(tm[3] & lt);
-      out += __popc(tm[0]) + __popc(tm[1]) + __popc(tm[2]) + __popc(tm[3]);
-      if (take[0] || take[1] || take[2] || take[3]) {
-        const int pos = base + i - n1p;   // all four on one page
-        const int slot = slot_of(pos);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (take[u]) {
-            lp[at] = pos + u;
-            le[at] = make_int2(slot + u, (int)((k[u] & 0x80000000u) ? k[u] ^ 0x80000000u : ~k[u]));
-            if (M == kCandidates && tail_n <= NT && k[u] < tail_end) {
-              const int i = atomicAdd(of(&listed_total, 0), 1);   // in any order: they are ranked below
-              of(list, 0)[i] = k[u];
-              of(every, 0)[i] = (uint32_t)at;
+          for (int u = 0; u < 4; ++u)
+            if (k[u] == T) {
+              if (!c) take[u] = before < need;
+              else if (before == need - 1 && ties_c < all[1]) rec[2] = i + u + 1;
+              ++before;
             }
-            ++at;
-          }
+          eq += sum;
+        }
+        unsigned tm[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) tm[u] = __ballot_sync(0xffffffffu, take[u]);
+        if ((tm[0] | tm[1] | tm[2] | tm[3]) == 0u) continue;
+        int at = out + __popc(tm[0] & lt) + __popc(tm[1] & lt) + __popc(tm[2] & lt) + __popc(tm[3] & lt);
+        out += __popc(tm[0]) + __popc(tm[1]) + __popc(tm[2]) + __popc(tm[3]);
+        if (take[0] || take[1] || take[2] || take[3]) {
+          const int pos = base + i - n1p;   // all four on one page
+          const int slot = slot_of(pos);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (take[u] && at < room) {
+              lp[at] = pos + u;
+              le[at] = make_int2(slot + u, (int)((k[u] & 0x80000000u) ? k[u] ^ 0x80000000u : ~k[u]));
+              if (M == kCandidates && tail_n <= NT && k[u] < tail_end) {
+                const int o = atomicAdd(of(&listed_total, 0), 1);   // in any order: they are ranked below
+                if (o < NT) {
+                  of(list, 0)[o] = k[u];
+                  of(every, 0)[o] = (uint32_t)at;
+                }
+              }
+              ++at;
+            }
+        }
       }
-    }
     };
     if (items <= cap) emit(Yes());
     else emit(No());
@@ -849,7 +855,7 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
     if (!CL) __syncthreads();
     if (rank != 0) return;
     int2* out = tail + (size_t)h * (kPagedTail + 1);
-    const int m = bad ? 0 : listed_total, n_t = min(m, kPagedTail);
+    const int m = bad ? 0 : min(listed_total, NT), n_t = min(m, kPagedTail);
     if (tid < m) {
       const uint32_t k = list[tid], i = every[tid];
       const uint64_t mine_last = last_first(k, i);
@@ -868,7 +874,7 @@ cudaError_t launch_select_t(const PagedPlan& P, int n_rows, int n, int C, int ca
                             cudaStream_t s) {
   const int seg = ((n + C - 1) / C + 3) & ~3;
   int page_cap = (seg >> P.page_shift) + 2;
-  if (page_cap > 4096) page_cap = 4096;
+  if (page_cap > 4100) page_cap = 4100;   // 65536 positions in the smallest pages
   const size_t smem = (size_t)(cap + page_cap) * 4;
   const cudaError_t e = ensure_smem_limit(paged_select_kernel<M, NT, SIEVE, CL>, (int)smem);
   if (e != cudaSuccess) return e;

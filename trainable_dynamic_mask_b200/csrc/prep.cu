@@ -17,7 +17,7 @@ namespace {
 
 // Dense outputs [B, heads, N, D].
 struct DenseDest {
-  static constexpr int kDepth = 4, kPerSm = 3;
+  static constexpr int kDepth = 4;
   struct Token {
     int position;
     unsigned b, n;
@@ -37,6 +37,13 @@ struct DenseDest {
   }
   DMA_DEVINL size_t step(int) const { return (size_t)N * D; }
 };
+
+template <typename T, int D, bool INTER>
+__global__ void __launch_bounds__(kRwThreads, 3)
+prep_fwd_kernel(const __grid_constant__ PrepArgs a, const __grid_constant__ DenseDest dest, int wt) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  walk_rows<T, D, INTER>(a, dest, wt, blockIdx.x, gridDim.x, smem);
+}
 
 template <typename T> constexpr int bwd_rows() { return sizeof(T) == 2 ? 4 : 2; }
 // a row's gradient, and its input or (values) the gate's share
@@ -145,7 +152,7 @@ prep_bwd_kernel(const __grid_constant__ PrepArgs a, int wt) {
       dst += RPW * sh;
     }
   };
-  Ring::run(Walk(a, RPW * U, wt), ring_smem, send, ready, work);
+  Ring::run(Walk(a, RPW * U, wt, blockIdx.x, gridDim.x), ring_smem, send, ready, work);
   // the block's partial sums of dg, one row of the workspace each, in the ring's place
   float* red = reinterpret_cast<float*>(ring_smem);   // [kRwWarps * RPW][D]
   static_assert(Ring::kBytes >= kRwWarps * RPW * D * 4, "the sums fit into the ring");
@@ -199,7 +206,14 @@ cudaError_t launch_fwd(const PrepArgs& a, cudaStream_t s) {
   d.positions = a.positions;
   d.N = (unsigned)a.N;
   d.H = a.H; d.Hkv = a.Hkv; d.D = D; d.size = (int)sizeof(T); d.first = a.first;
-  return launch_row_walk<T, D>(a, d, s);
+  int wt;
+  const int blocks = walk_blocks((long long)a.B * a.N, 3, &wt);
+  constexpr int smem = FwdRing<T, DenseDest::kDepth>::kBytes;
+  auto kernel = a.inter ? prep_fwd_kernel<T, D, true> : prep_fwd_kernel<T, D, false>;
+  const cudaError_t e = ensure_smem_limit(kernel, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<blocks, kRwThreads, smem, s>>>(a, d, wt);
+  return cudaGetLastError();
 }
 
 template <typename T, int D>

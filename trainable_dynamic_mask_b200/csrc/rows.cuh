@@ -172,12 +172,13 @@ struct Walk {
   unsigned tok, tokens, step;
   unsigned b, n, N, step_b, step_n;   // the token as (batch row, position)
   int chunk, first, chunks, wt, cq, ck;
-  DMA_DEVINL Walk(const PrepArgs& a, int per_chunk, int wt_) : wt(wt_) {
+  // block of blocks share the tokens
+  DMA_DEVINL Walk(const PrepArgs& a, int per_chunk, int wt_, unsigned block, unsigned blocks) : wt(wt_) {
     const int warp = threadIdx.x >> 5;
     N = (unsigned)a.N;
     tokens = (unsigned)a.B * N;
-    step = gridDim.x * (kRwWarps / wt);
-    tok = blockIdx.x * (kRwWarps / wt) + warp / wt;
+    step = blocks * (kRwWarps / wt);
+    tok = block * (kRwWarps / wt) + warp / wt;
     b = tok / N;
     n = tok - b * N;
     step_b = step / N;
@@ -276,19 +277,17 @@ template <typename T, int DEPTH> using FwdRing = RowRing<sizeof(T) / 2, fwd_rows
 // Queries and keys normed and rotated, values copied, from the projections (a.in, a.stride) to where Dest
 // says: dest.enter(at, token) (every lane of the warp) is false if nothing of the token is written,
 // else token.position is its position and dest.row(part, token) the address of its first head's row, heads
-// dest.step(part) elements apart.  Dest::kDepth chunks are in flight, Dest::kPerSm
-// CTAs on an SM.
+// dest.step(part) elements apart.  Dest::kDepth chunks are in flight.  By a block of kRwThreads, with
+// FwdRing<T, Dest::kDepth>::kBytes of shared memory at ring_smem.
 template <typename T, int D, bool INTER, typename Dest>
-__global__ void __launch_bounds__(kRwThreads, 3)
-row_walk_kernel(const __grid_constant__ PrepArgs a, const __grid_constant__ Dest dest, int wt) {
+DMA_DEVINL void walk_rows(const PrepArgs& a, const Dest& dest, int wt, unsigned block, unsigned blocks,
+                          unsigned char* ring_smem) {
   constexpr int L = D / 8, RPW = 32 / L, U = fwd_rows<T>();
   using Ring = FwdRing<T, Dest::kDepth>;
-  extern __shared__ __align__(128) unsigned char ring_smem[];
   __shared__ __align__(16) float2 tab[kRwWarps][D / 2 + kTabPad];
   __shared__ uint64_t rate[D / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = lane / L, e = (lane % L) * 8;
   const bool upper = e >= a.rot >> 1;
-  pdl_trigger();
   auto ready = [&]() {
     for (int k = threadIdx.x; k < a.rot >> 1; k += kRwThreads) rate[k] = turn_rate(__ldg(a.inv_freq + k));
     if (lane < kTabPad) tab[warp][D / 2 + lane] = make_float2(1.f, 0.f);
@@ -347,18 +346,7 @@ row_walk_kernel(const __grid_constant__ PrepArgs a, const __grid_constant__ Dest
       dst += RPW * sh;
     }
   };
-  Ring::run(Walk(a, RPW * U, wt), ring_smem, send, ready, work);
-}
-
-template <typename T, int D, typename Dest>
-cudaError_t launch_row_walk(const PrepArgs& a, const Dest& dest, cudaStream_t s) {
-  int wt;
-  const int blocks = walk_blocks((long long)a.B * a.N, Dest::kPerSm, &wt);
-  auto kernel = a.inter ? row_walk_kernel<T, D, true, Dest> : row_walk_kernel<T, D, false, Dest>;
-  const cudaError_t e = ensure_smem_limit(kernel, FwdRing<T, Dest::kDepth>::kBytes);
-  if (e != cudaSuccess) return e;
-  kernel<<<blocks, kRwThreads, FwdRing<T, Dest::kDepth>::kBytes, s>>>(a, dest, wt);
-  return cudaGetLastError();
+  Ring::run(Walk(a, RPW * U, wt, block, blocks), ring_smem, send, ready, work);
 }
 
 }  // namespace dma
