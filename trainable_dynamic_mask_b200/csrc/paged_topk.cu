@@ -175,7 +175,7 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
   __shared__ int2 batch_in[SIEVE ? kPsMaxBatches : 1];    // keys above and at the edge, then those in front
   __shared__ int listed_total;
   __shared__ int wbuf[5][NW];
-  __shared__ int found_bin, found_above, found_count;
+  __shared__ int found_bin, found_above, found_count, other_bin, other_above;
   __shared__ uint32_t found_key;
   cg::cluster_group cl = cg::this_cluster();
   constexpr int kMost = CL ? kPsMaxCluster : 1;
@@ -240,7 +240,7 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
     sh.members = 0;
     msh = sh;
     listed_total = 0;
-    found_bin = found_above = found_count = 0;
+    found_bin = found_above = found_count = other_bin = other_above = 0;
     found_key = 0u;
   }
   *reinterpret_cast<int4*>(hist + 4 * tid) = make_int4(0, 0, 0, 0);
@@ -295,8 +295,9 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
   };
 
   // the counter (of 4 NT, summed over the cluster) that holds the want-th largest key, `above` keys lying
-  // above all of them: found_bin, found_above, found_count
-  auto find_bin = [&](int* counts, int above, int want, int* buf) {
+  // above all of them: found_bin, found_above, found_count; and (other > 0) the one that holds the other-th:
+  // other_bin, other_above
+  auto find_bin = [&](int* counts, int above, int want, int* buf, int other = 0) {
     // thread t sums counters 4 t' .. 4 t' + 3, t' = NT - 1 - t: from the top
     const int b4 = (NT - 1 - tid) * 4;
     int4 c = make_int4(0, 0, 0, 0);
@@ -318,19 +319,30 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
       if (lane >= o) incl += v;
     }
     const int excl = above + warps_before<NW>(__shfl_sync(0xffffffffu, incl, 31), buf).x + incl - mine;
-    if (excl < want && excl + mine >= want) {   // one thread of the block
-      int bin = b4 + 3, up = excl, here = c.w;
+    auto within = [&](int k, int& bin, int& up, int& here) {   // the counter of this thread that holds the k-th
+      bin = b4 + 3;
+      up = excl;
+      here = c.w;
       const int cc[3] = {c.z, c.y, c.x};
 #pragma unroll
       for (int u = 0; u < 3; ++u)
-        if (up + here < want) {
+        if (up + here < k) {
           up += here;
           here = cc[u];
           --bin;
         }
+    };
+    int bin, up, here;
+    if (excl < want && excl + mine >= want) {   // one thread of the block
+      within(want, bin, up, here);
       found_bin = bin;
       found_above = up;
       found_count = here;
+    }
+    if (M == kCandidates && excl < other && excl + mine >= other) {
+      within(other, bin, up, here);
+      other_bin = bin;
+      other_above = up;
     }
     __syncthreads();
   };
@@ -594,23 +606,13 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
         if (k >= lo && k - lo <= span) atomicAdd(&hist[(k - lo) >> shift], 1);
       });
       all_sync();
-      find_bin(hist, above, W, wbuf[0]);
-      if constexpr (M == kCandidates) {
-        if (tail_end == 0u) {
-          // the counter of the kPagedTail-th key from the edge: the last candidates are those below its end
-          const int bin = found_bin, up = found_above, here = found_count;
-          __syncthreads();
-          find_bin(hist, 0, max(1, W - kPagedTail + 1), wbuf[0]);
-          tail_n = W - found_above;
-          tail_end = lo + (((uint64_t)found_bin + 1u) << shift);
-          __syncthreads();
-          if (tid == 0) {
-            found_bin = bin;
-            found_above = up;
-            found_count = here;
-          }
-          __syncthreads();
-        }
+      // (candidates) the first time, also the counter of the kPagedTail-th key from the edge: the last candidates
+      // are those below its end
+      const bool first = M == kCandidates && tail_end == 0u;
+      find_bin(hist, above, W, wbuf[0], first ? max(1, W - kPagedTail + 1) : 0);
+      if (first) {
+        tail_n = W - other_above;
+        tail_end = lo + (((uint64_t)other_bin + 1u) << shift);
       }
       above = found_above;
       lo += (uint32_t)found_bin << shift;
@@ -623,12 +625,20 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
           if (k >= lo && k - lo <= span) list[min(atomicAdd(&sh.members, 1), NT - 1)] = k;
         });
         all_sync();
-        int m = 0;
-        for (int r = 0; r < C; ++r) {
-          const int mr = min(of(&sh, r)->members, NT - m);
-          if (tid < mr) every[m + tid] = *of(list + tid, r);
+        // each thread one of them: whose list it is in, and where
+        int members[kMost], m = 0, from = -1, at = 0;
+#pragma unroll
+        for (int r = 0; r < kMost; ++r) members[r] = r < C ? of(&sh, r)->members : 0;
+#pragma unroll
+        for (int r = 0; r < kMost; ++r) {
+          const int mr = min(members[r], NT - m);
+          if (tid >= m && tid < m + mr) {
+            from = r;
+            at = tid - m;
+          }
           m += mr;
         }
+        if (from >= 0) every[tid] = *of(list + at, from);
         __syncthreads();
         if (tid < m) {
           const uint32_t k = every[tid];
