@@ -178,44 +178,49 @@ def cp_compact(p, prefix_len, n_prev, cands, delta, K, V, delta_c, Kc, Vc, pos_c
 
 # ---------------------------------------------------------------- projections to inputs
 
-def _storage(p):
-    """torch type of p's storage."""
-    import torch
-    return torch.bfloat16 if p.dtype == DMA_BF16 else torch.float32
+class _Torch:
+    """What every call needs of torch, looked up once (a small call takes about as long as its checks)."""
+    ready = False
 
-
-def _stream_on(stream, dev):
-    """_stream, for the current device dev.  The address alone: a Stream object takes longer to make than
-    all of a small call's checks."""
-    if stream is None:
+    @classmethod
+    def get(cls):
         import torch
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return _stream(stream)
+        torch.cuda.current_device()   # CUDA is up, or this says why not
+        cls.types = {DMA_BF16: torch.bfloat16, DMA_F32: torch.float32}
+        cls.f32, cls.i32 = torch.float32, torch.int32
+        cls.device = staticmethod(torch._C._cuda_getDevice)
+        cls.stream = staticmethod(torch._C._cuda_getCurrentRawStream)   # its address: no Stream object is made
+        cls.ready = True
+        return cls
+
+
+def _torch():
+    return _Torch if _Torch.ready else _Torch.get()
 
 
 def _dense(name, t, shape, dtype, dev):
     """Address of a dense tensor of that shape and type on the current device dev (None: NULL)."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-        _refuse(name, t, shape, dtype, dev)
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(name, t, shape, dtype, dev)
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _rows(name, t, shape, dtype, dev, out):
-    """Address of rows [.., heads, d] at any strides; the strides of all but the channels go into out."""
+    """Address of rows [B, N, heads, d] (or [T, heads, d]) at any strides; those of all but the channels go
+    into out (of a dimension of one element, which has no stride to speak of, 0)."""
     if t is None:
         return None
     st = t.stride()
     if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or st[-1] != 1:
         _refuse(name, t, shape, dtype, dev)
         raise ValueError(f"{name}: the channels of a row must be contiguous")
-    # a dimension of one element has no stride to speak of
-    out[2] = st[-2] if shape[-2] > 1 else 0
-    out[1] = st[-3] if shape[-3] > 1 else 0
-    if len(shape) == 4:
-        out[0] = st[0] if shape[0] > 1 else 0
+    if len(st) == 4:
+        out[:] = (st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0, st[2] if shape[2] > 1 else 0)
+    else:
+        out[:] = (0, st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0)
     return t.data_ptr()
 
 
@@ -248,12 +253,12 @@ def _check_prep_tensors(p, r, dev):
     """The weights and positions of r fit p (looked at again when p's sizes change)."""
     key = (p.B, p.N, p.d, p.dtype, dev)
     if r.fits != key:
-        import torch
+        tt = _torch()
         freq, qw, kw, pos = r.tensors
-        _dense("inv_freq", freq, (r.rot // 2,), torch.float32, dev)
-        _dense("q_weight", qw, (p.d,), _storage(p), dev)
-        _dense("k_weight", kw, (p.d,), _storage(p), dev)
-        _dense("positions", pos, (p.B, p.N), torch.int32, dev)
+        _dense("inv_freq", freq, (r.rot // 2,), tt.f32, dev)
+        _dense("q_weight", qw, (p.d,), tt.types[p.dtype], dev)
+        _dense("k_weight", kw, (p.d,), tt.types[p.dtype], dev)
+        _dense("positions", pos, (p.B, p.N), tt.i32, dev)
         r.fits = key
 
 
@@ -261,16 +266,15 @@ def prep(p, r, q, k, v, Q, K, V, stream=None):
     """Projections q [B, N, H, d], k, v [B, N, Hkv, d] (any strides) to the attention's inputs
     Q [B, H, N, d], K, V [B, Hkv, N, d]: per-head norm, rotation and transposition in one pass.
     v and V may be None together."""
-    import torch
-    call = load().dma_prep
-    dev, t = torch.cuda.current_device(), _storage(p)
+    call, tt = load().dma_prep, _torch()
+    dev, t = tt.device(), tt.types[p.dtype]
     B, H, Hkv, N, d = p.B, p.H, p.Hkv, p.N, p.d
     _check_prep_tensors(p, r, dev)
     st = DmaPrepStrides()
     check("dma_prep", call(
         p, r, st, _rows("q", q, (B, N, H, d), t, dev, st.q), _rows("k", k, (B, N, Hkv, d), t, dev, st.k),
         _rows("v", v, (B, N, Hkv, d), t, dev, st.v), _dense("Q", Q, (B, H, N, d), t, dev),
-        _dense("K", K, (B, Hkv, N, d), t, dev), _dense("V", V, (B, Hkv, N, d), t, dev), _stream_on(stream, dev)))
+        _dense("K", K, (B, Hkv, N, d), t, dev), _dense("V", V, (B, Hkv, N, d), t, dev), tt.stream(dev) if stream is None else _stream(stream)))
 
 
 def prep_workspace_size(p, r) -> int:
@@ -283,9 +287,8 @@ def prep_bwd(p, r, q, k, dQ, dK, dV, dV_gate, dq, dk, dv, dq_weight, dk_weight, 
     """Gradients of prep's inputs from those of its outputs: dq, dk, dv are written at their own
     strides ([B, N, heads, d]), dV_gate (float32, or None) is added to dV, dq_weight and dk_weight are
     float32 [d] (None: not wanted); q, k as in prep (None where there is no weight)."""
-    import torch
-    call = load().dma_prep_bwd
-    dev, t, f = torch.cuda.current_device(), _storage(p), torch.float32
+    call, tt = load().dma_prep_bwd, _torch()
+    dev, t, f = tt.device(), tt.types[p.dtype], tt.f32
     B, H, Hkv, N, d = p.B, p.H, p.Hkv, p.N, p.d
     _check_prep_tensors(p, r, dev)
     st, gst = DmaPrepStrides(), DmaPrepStrides()
@@ -295,11 +298,14 @@ def prep_bwd(p, r, q, k, dQ, dK, dV, dV_gate, dq, dk, dv, dq_weight, dk_weight, 
         _dense("dK", dK, hk, t, dev), _dense("dV", dV, hk, t, dev), _dense("dV_gate", dV_gate, hk, f, dev),
         _rows("dq", dq, sq, t, dev, gst.q), _rows("dk", dk, sk, t, dev, gst.k), _rows("dv", dv, sk, t, dev, gst.v),
         _dense("dq_weight", dq_weight, (d,), f, dev), _dense("dk_weight", dk_weight, (d,), f, dev),
-        _workspace(workspace, dev), _nbytes(workspace), _stream_on(stream, dev)))
+        _workspace(workspace, dev), _nbytes(workspace), tt.stream(dev) if stream is None else _stream(stream)))
 
 
 def _workspace(ws, dev):
-    if ws is not None and ws.get_device() != dev:
+    """Address of a workspace on the current device dev."""
+    if ws is None:
+        return None
+    if ws.get_device() != dev:
         raise ValueError(f"the workspace must be on the current device (cuda:{dev}), not {ws.device}")
     return _ptr(ws)
 
@@ -311,16 +317,16 @@ def make_pages(p, K, V, delta, table, lens, prefix=0) -> DmaPages:
     [n_pages, H, page] float32, table int32 [B, max_pages], lens int32 [B] (device tensors, which the
     result keeps alive; they may be written to between calls).  prefix: leading positions that every
     sequence shares, a multiple of the page length."""
-    import torch
     if K.dim() != 4 or table.dim() != 2:
         raise ValueError("K must be [n_pages, Hkv, page, d] and table [B, max_pages]")
-    dev, t = torch.cuda.current_device(), _storage(p)
+    tt = _torch()
+    dev, t = tt.device(), tt.types[p.dtype]
     n, page = K.shape[0], K.shape[2]
     rows = (n, p.Hkv, page, p.d)
     c = DmaPages(K=_dense("K", K, rows, t, dev), V=_dense("V", V, rows, t, dev),
-                 delta=_dense("delta", delta, (n, p.H, page), torch.float32, dev),
-                 table=_dense("table", table, (p.B, table.shape[1]), torch.int32, dev),
-                 lens=_dense("lens", lens, (p.B,), torch.int32, dev), n_pages=n, page=page,
+                 delta=_dense("delta", delta, (n, p.H, page), tt.f32, dev),
+                 table=_dense("table", table, (p.B, table.shape[1]), tt.i32, dev),
+                 lens=_dense("lens", lens, (p.B,), tt.i32, dev), n_pages=n, page=page,
                  max_pages=table.shape[1], prefix=int(prefix))
     c.tensors, c.device = (K, V, delta, table, lens), dev
     return c
@@ -342,41 +348,38 @@ def paged_append(p, c, r, q, k, v, Delta, A, Q, workspace, starts=None, stream=N
     as the last positions of c.lens: K normed and rotated, V, the gate values; Q [T, H, d] receives the
     normed and rotated queries (q and Q may be None together).  starts: device int32 [B + 1], the
     sequences' token ranges; None: one token each."""
-    import torch
-    call = load().dma_paged_append
-    dev, t, f = torch.cuda.current_device(), _storage(p), torch.float32
+    call, tt = load().dma_paged_append, _torch()
+    dev, t, f = tt.device(), tt.types[p.dtype], tt.f32
     T, H, Hkv, d = k.shape[0], p.H, p.Hkv, p.d
     _same_device(c, dev)
     _check_prep_tensors(p, r, dev)
     st = DmaPrepStrides()
     check("dma_paged_append", call(
-        p, c, r, st, T, _dense("starts", starts, (p.B + 1,), torch.int32, dev),
+        p, c, r, st, T, _dense("starts", starts, (p.B + 1,), tt.i32, dev),
         _rows("q", q, (T, H, d), t, dev, st.q), _rows("k", k, (T, Hkv, d), t, dev, st.k),
         _rows("v", v, (T, Hkv, d), t, dev, st.v), _dense("Delta", Delta, (Hkv * d, H), t, dev),
         _dense("A", A, (H,), f, dev), _dense("Q", Q, (T, H, d), t, dev), _workspace(workspace, dev),
-        _nbytes(workspace), _stream_on(stream, dev)))
+        _nbytes(workspace), tt.stream(dev) if stream is None else _stream(stream)))
 
 
 def paged_topk(p, c, workspace, stream=None):
     """Selection of every (sequence, head) over its cache, into the workspace."""
-    import torch
-    call = load().dma_paged_topk
-    dev = torch.cuda.current_device()
+    call, tt = load().dma_paged_topk, _torch()
+    dev = tt.device()
     _same_device(c, dev)
     check("dma_paged_topk", call(p, c, _workspace(workspace, dev), _nbytes(workspace),
-                                                  _stream_on(stream, dev)))
+                                                  tt.stream(dev) if stream is None else _stream(stream)))
 
 
 def paged_attn(p, c, Q, workspace, O, LSE, stream=None):
     """Attention of one query [B, H, d] for each sequence over the keys paged_topk selected."""
-    import torch
-    call = load().dma_paged_attn
-    dev, t = torch.cuda.current_device(), _storage(p)
+    call, tt = load().dma_paged_attn, _torch()
+    dev, t = tt.device(), tt.types[p.dtype]
     shape = (p.B, p.H, p.d)
     _same_device(c, dev)
     check("dma_paged_attn", call(
         p, c, _dense("Q", Q, shape, t, dev), _workspace(workspace, dev), _nbytes(workspace),
-        _dense("O", O, shape, t, dev), _dense("LSE", LSE, (p.B, p.H), torch.float32, dev), _stream_on(stream, dev)))
+        _dense("O", O, shape, t, dev), _dense("LSE", LSE, (p.B, p.H), tt.f32, dev), tt.stream(dev) if stream is None else _stream(stream)))
 
 
 # ---------------------------------------------------------------- convenience (torch allocation)
