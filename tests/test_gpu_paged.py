@@ -497,6 +497,18 @@ def test_append(name, layout):
         assert c.torch.equal(x, y)
 
 
+@pytest.mark.parametrize("B", [31, 32, 33, 70])
+def test_append_to_many_sequences(B):
+    """Sequences are looked up in two ways, for fewer than 32 and for more; some append nothing."""
+    cnt = [(7 * b) % 5 if b % 3 else 0 for b in range(B)]
+    c = Cache([n + 3 * b % 40 for b, n in enumerate(cnt)], 4, 2, 64, 16, "bf16", 8, seed=B, N=64)
+    a = _append(c, cnt, 64, False, True, pad=37)
+    before = [x.clone() for x in (c.K, c.V, c.delta)]
+    c.dma.paged_append(c.p, c.c, a["r"], a["q"], a["k"], a["v"], a["Delta"], a["A"], a["Q"], c.ws, starts=a["starts"])
+    _check_append(c, a, 64, False, before)
+    assert c.dma.check_device_status(c.p, c.ws) == 0
+
+
 def test_append_skips_what_has_no_place():
     c = Cache([30, 30, 30], 2, 1, 64, 16, "bf16", 8, N=32, seed=8)
     dma, torch = c.dma, c.torch

@@ -4,8 +4,15 @@
 //
 // One kernel, two kinds of CTAs side by side: the first walk over the rows (rows.cuh, as in prep.cu), the
 // others form the gate's product (the values of 16 tokens against Delta, tensor cores for bf16).  The walk's
-// shares are fixed when it starts and it is the longer way, so it comes first, with two CTAs an SM; the
-// gate's CTAs follow one another in the place that is left.
+// shares are fixed when it starts and it is the longer way, so it comes first, with three CTAs an SM and two
+// chunks of rows on their way; the gate's CTAs follow where those have ended.
+//
+// Bytes: each projection read once and each row written once, 16 KB a token at 16 + 8 + 8 heads of 128
+// channels in bf16, Delta from L2.  5037 tokens of 5 prompts take 25.7 us (3.2 TB/s); without the gate they
+// would take 4 us less, the gate alone 9.  What is left is a short call's: a plain copy of as many bytes
+// stays a third below its rate for long ones.  Two CTAs an SM with four chunks on their way took 28.6 us,
+// three with four 27.5, four (64 registers) 29; the gate's CTAs first, or with four stages, the same.
+// One token of a sequence (8 rows) takes 5 us, bound by latency: the lookup's reads, one wave of rows, the gate.
 #include "rows.cuh"
 
 namespace dma {
@@ -19,24 +26,48 @@ struct Place {
   int page, slot;
 };
 
-// Sequence and slot of token t < T (each lane its own).
-DMA_DEVINL Place place_of(const PagedPlan& P, const PagedAppendArgs& a, int t, int32_t* status) {
-  int seq = t, first = t, n = 1;
-  if (a.starts != nullptr) {
+// Sequence and slot of token t (a whole warp, each lane its own token; wanted: t < T).  What is read first
+// depends on nothing, the page number on that: up to 31 sequences' starts and lengths are read at once, a
+// sequence a lane, rather than searched for one after the other.
+DMA_DEVINL Place place_of(const PagedPlan& P, const PagedAppendArgs& a, int t, bool wanted, int32_t* status) {
+  constexpr unsigned kAll = 0xffffffffu;
+  int seq = t, first = t, n = 1, len = 0;
+  if (a.starts == nullptr) {
+    if (wanted) len = __ldg(P.lens + seq);
+  } else {
     // the sequence before the first that starts behind t; none: padding in front of them all, or behind
     int lo = 0, hi = P.B + 1;   // starts[i] <= t for i < lo, > t for i >= hi
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(a.starts + mid) <= t) lo = mid + 1;
-      else hi = mid;
+    if (P.B < 32) {
+      const int lane = threadIdx.x & 31;
+      const int s = __ldg(a.starts + min(lane, P.B)), l = __ldg(P.lens + min(lane, P.B - 1));
+#pragma unroll
+      for (int i = 0; i < 6; ++i) {   // 33 answers at most
+        const int mid = (lo + hi) >> 1, v = __shfl_sync(kAll, s, mid & 31);
+        if (lo < hi) {
+          if (v <= t) lo = mid + 1;
+          else hi = mid;
+        }
+      }
+      seq = lo - 1;
+      first = __shfl_sync(kAll, s, seq & 31);
+      n = __shfl_sync(kAll, s, (seq + 1) & 31) - first;
+      len = __shfl_sync(kAll, l, seq & 31);
+    } else if (wanted) {
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(a.starts + mid) <= t) lo = mid + 1;
+        else hi = mid;
+      }
+      seq = lo - 1;
+      if (seq >= 0 && seq < P.B) {
+        first = __ldg(a.starts + seq);
+        n = __ldg(a.starts + seq + 1) - first;
+        len = __ldg(P.lens + seq);
+      }
     }
-    seq = lo - 1;
     if (seq < 0 || seq >= P.B) return {0, -1, 0, 0};
-    first = __ldg(a.starts + seq);
-    n = __ldg(a.starts + seq + 1) - first;
   }
-  const int len = __ldg(P.lens + seq);
-  if (len <= 0) return {seq, -1, 0, 0};
+  if (!wanted || len <= 0) return {seq, -1, 0, 0};
   const int pos = len - n + (t - first);
   int page = -1;
   if (pos >= 0 && pos < len && len <= P.N) page = __ldg(P.table + (size_t)seq * P.max_pages + (pos >> P.page_shift));
@@ -52,7 +83,7 @@ DMA_DEVINL Place place_of(const PagedPlan& P, const PagedAppendArgs& a, int t, i
 // Keys and values to their slots, queries to Q [T, H, D].  A warp looks up the places of its next 32 tokens
 // together, a token a lane: the lookups' three or more dependent reads are then paid once.
 struct SlotDest {
-  static constexpr int kDepth = 4;
+  static constexpr int kDepth = 2;
   struct Token {
     int position;
     unsigned tok;
@@ -68,8 +99,7 @@ struct SlotDest {
     const int i = t.looked_up & 31;
     if (i == 0) {
       const unsigned mine = at.tok + (threadIdx.x & 31) * at.step;
-      Place pl = {0, -1, 0, 0};
-      if (mine < at.tokens && mine >= at.tok) pl = place_of(P, a, (int)mine, status);
+      const Place pl = place_of(P, a, (int)mine, mine < at.tokens && mine >= at.tok, status);
       __syncwarp();
       t.pos = pl.pos;
       t.page = pl.page;
@@ -98,10 +128,9 @@ constexpr int kAgWarps = kAgThreads / 32;
 DMA_DEVINL void gate_places(const PagedPlan& P, const PagedAppendArgs& a, int t0, int n, long long* where,
                             int32_t* status) {
   const int i = threadIdx.x;
-  if (i < n) {
-    Place pl = {0, -1, 0, 0};
-    if (t0 + i < a.T) pl = place_of(P, a, t0 + i, status);
-    where[i] = pl.pos < 0 ? -1 : ((long long)pl.page * P.H << P.page_shift) + pl.slot;
+  if (i < 32) {
+    const Place pl = place_of(P, a, t0 + i, i < n && t0 + i < a.T, status);
+    if (i < n) where[i] = pl.pos < 0 ? -1 : ((long long)pl.page * P.H << P.page_shift) + pl.slot;
   }
 }
 
@@ -285,7 +314,7 @@ paged_append_kernel(const __grid_constant__ PrepArgs w, const __grid_constant__ 
 template <typename T, int D, int HT>
 cudaError_t launch_append(const PrepArgs& w, const SlotDest& d, cudaStream_t s) {
   int wt;
-  const int row_blocks = walk_blocks(d.a.T, 2, &wt), tok = HT > 0 ? kAgTok : kAfTok;
+  const int row_blocks = walk_blocks(d.a.T, 3, &wt), tok = HT > 0 ? kAgTok : kAfTok;
   constexpr int smem = append_smem<T, HT>();
   auto kernel = w.inter ? paged_append_kernel<T, D, true, HT> : paged_append_kernel<T, D, false, HT>;
   const cudaError_t e = ensure_smem_limit(kernel, smem);

@@ -23,6 +23,10 @@ namespace {
 
 DMA_DEVINL float exp_diff(float x, float m) { return fast_exp2((x - m) * kLog2e); }
 
+// A slot of the cache; what the selection wrote always is one, a workspace it has not been run on may hold
+// anything, which must not be followed.
+DMA_DEVINL int inside(int slot, int n_slots) { return (unsigned)slot < (unsigned)n_slots ? slot : 0; }
+
 // Writes the row's output from its sums: nothing kept: 0 and -inf; a NaN stays.
 template <typename T> DMA_DEVINL void put_channel(T* O, float o, float l) {
   store_from_f32(O, l > 0.f ? o / l : (l == 0.f ? 0.f : l));
@@ -75,7 +79,7 @@ __global__ void __launch_bounds__(NT, 512 / NT)
 paged_list_kernel(const T* __restrict__ Q, const T* __restrict__ K, const T* __restrict__ V,
                   const int4* __restrict__ rows, const int2* __restrict__ ent, float* __restrict__ part,
                   int32_t* __restrict__ counters, T* __restrict__ O, float* __restrict__ LSE, int H, int Hkv,
-                  int page_shift, int sel_len, int n_split, int n_psplit, float scale) {
+                  int page_shift, int n_slots, int sel_len, int n_split, int n_psplit, float scale) {
   constexpr int L = D / 8, RPW = 32 / L, NG = (NT / 32) * RPW;   // lanes of a row; groups of a warp, of the CTA
   constexpr int U = list_keys<T>(), NP = sizeof(T) / 2;         // 16-byte pieces of a lane's eight channels
   constexpr int E = kPagedSplit / NG / L;                       // entries of a lane
@@ -99,6 +103,7 @@ paged_list_kernel(const T* __restrict__ Q, const T* __restrict__ K, const T* __r
     const int k = (lane % L + i * L) * NG + grp;
     en[i] = make_int2(0, 0);
     if (k < nk) en[i] = list[k];
+    en[i].x = inside(en[i].x, n_slots);
   }
   // the entry of the group's key j
   auto entry = [&](int j) {
@@ -282,7 +287,7 @@ template <int D, int R>
 __global__ void __launch_bounds__(cand_threads<R>(), 2)
 paged_cand_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ K, const uint16_t* __restrict__ V,
                   const int4* __restrict__ rows, const int32_t* __restrict__ crow, const int2* __restrict__ cent,
-                  float* __restrict__ part, int B, int H, int Hkv, int page_shift, int cand_len, int cand_split,
+                  float* __restrict__ part, int B, int H, int Hkv, int page_shift, int n_slots, int cand_len, int cand_split,
                   int n_part, float scale) {
   constexpr int kPcThreads = cand_threads<R>(), kPcWarps = kPcThreads / 32;
   constexpr int CH = D / 8, KG = kPcWarps / R, NT = 8 / KG, NO = D / 8;   // NT, NO: 8-wide tiles of keys, channels
@@ -305,7 +310,7 @@ paged_cand_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ K
   for (int i = tid; i < nt * kPcTile; i += kPcThreads) {
     int2 e = make_int2(0, 0);
     if (i < nc) e = cent[(size_t)h * cand_len + c0 + i];
-    cslot[i] = e.x;
+    cslot[i] = inside(e.x, n_slots);
     cdel[i] = __int_as_float(e.y);
     ckey[i] = i < nc ? order_key(__int_as_float(e.y)) : 0u;
   }
@@ -534,7 +539,7 @@ cudaError_t launch_cand(const PagedPlan& P, const void* Q, void* ws, cudaStream_
       paged_cand_kernel<D, R>, dim3(P.n_psplit, P.H, (P.B + 16 * R - 1) / (16 * R)), cand_threads<R>(), cand_smem<D>(), s, 1,
       (const uint16_t*)Q, (const uint16_t*)P.K, (const uint16_t*)P.V, ws_ptr<int4>(ws, P.off_rows),
       ws_ptr<int32_t>(ws, P.off_crow), ws_ptr<int2>(ws, P.off_cent), ws_ptr<float>(ws, P.off_part), P.B, P.H, P.Hkv,
-      P.page_shift, P.cand_len, P.cand_split, P.n_psplit + P.n_split, P.scale);
+      P.page_shift, P.n_pages << P.page_shift, P.cand_len, P.cand_split, P.n_psplit + P.n_split, P.scale);
 }
 
 template <int D>
@@ -550,7 +555,7 @@ cudaError_t launch_list_t(const PagedPlan& P, const void* Q, void* ws, void* O, 
   if (e != cudaSuccess) return e;
   return launch_after(
       paged_list_kernel<T, D, NT>, dim3(P.n_split, P.B * P.H), NT, list_smem<T, NT>(), s, 1, (const T*)Q, (const T*)P.K, (const T*)P.V, ws_ptr<int4>(ws, P.off_rows), ws_ptr<int2>(ws, P.off_ent),
-      ws_ptr<float>(ws, P.off_part), ws_ptr<int32_t>(ws, P.off_count), (T*)O, LSE, P.H, P.Hkv, P.page_shift, P.sel_len,
+      ws_ptr<float>(ws, P.off_part), ws_ptr<int32_t>(ws, P.off_count), (T*)O, LSE, P.H, P.Hkv, P.page_shift, P.n_pages << P.page_shift, P.sel_len,
       P.n_split, P.n_psplit, P.scale);
 }
 
