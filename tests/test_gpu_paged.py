@@ -253,6 +253,17 @@ PREFIXED = {
     "constant": ([160, 170, 480], 160, 1, 1, 64, 32, "bf16", 80, dict(delta="constant")),
     "heads": ([512, 700, 513], 512, 4, 2, 64, 16, "bf16", 200, dict(w_heads=[200, 1, 0, 999])),
     "batch": ([4096 + i for i in range(70)], 4096, 4, 2, 128, 64, "bf16", 600, {}),
+    "batch_33": ([320 + 5 * (i % 9) for i in range(33)], 320, 3, 1, 64, 32, "bf16", 100, {}),
+    "batch_64": ([2048 + i % 50 for i in range(64)], 2048, 2, 2, 128, 64, "bf16", 1500, dict(w_heads=[1500, 513])),
+    "batch_65_ties": ([1024 + 3 * i for i in range(65)], 1024, 2, 1, 64, 64, "bf16", 400, dict(delta="levels")),
+    "batch_all": ([640 + i for i in range(40)], 640, 2, 1, 128, 64, "bf16", 900, {}),
+    "batch_small": ([0 if i % 7 == 3 else 16 + i for i in range(48)], 16, 2, 1, 128, 16, "bf16", 5, {}),
+    "many_33": ([1280 + 7 * (i % 9) for i in range(33)], 1280, 16, 4, 64, 64, "bf16", 1200, {}),
+    "many_ties": ([1024 + 3 * i for i in range(65)], 1024, 10, 2, 64, 64, "bf16", 1000, dict(delta="levels")),
+    "many_all": ([2432 + i for i in range(40)], 2432, 8, 8, 128, 64, "bf16", 3000, {}),
+    "many_130": ([0 if i % 7 == 3 else 1024 + i for i in range(130)], 1024, 8, 2, 128, 32, "bf16", 800, {}),
+    "many_windows": ([2048 + i for i in range(40)], 2048, 16, 2, 128, 64, "bf16", 1200,
+                     dict(w_heads=[1200, 1, 2, 64, 127, 128, 129, 256, 257, 511, 512, 513, 640, 1100, 1199, 3])),
     "long": ([40960, 50001], 40960, 2, 1, 128, 64, "bf16", 2048, {}),
     "crossing": ([4096, 4700, 4200, 4097, 4150], 4096, 2, 1, 64, 64, "bf16", 512, {}),
     "crossing_ties": ([1024 + 40 * i for i in range(12)], 1024, 2, 1, 64, 64, "bf16", 400, dict(delta="levels")),
@@ -316,6 +327,40 @@ def test_shared_prefix_masked_places_may_hold_anything():
         other = torch.arange(64, device="cuda") != 5
         assert (got[1][s, 0, other].float() - want[1][s, 0, other].float()).abs().max() <= 2.0 ** -8 * 4
     assert torch.equal(got[1][1], want[1][1]) and torch.equal(got[2], want[2])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,w", [(1, 700), (16, 1200)])
+def test_shared_prefix_of_many_masked_places_may_hold_anything(H, w, d):
+    """As above, for batches that fill both kernels: infinities in the first, a middle and the last tile."""
+    B, prefix = 40, 1280
+    c = Cache([prefix + 64] + [prefix + 1 + i for i in range(1, B - 1)] + [prefix + 1300], H, 1, d, 64, "bf16", w, seed=d,
+              prefix=prefix)
+    torch = c.torch
+    last = c.table[B - 1, 20:].long()
+    c.delta[last] = 2.0 + torch.rand(c.delta[last].shape, generator=c.gen, device="cuda")   # it selects none of the prefix
+    want = c.run()
+    sel = c.selected()
+    assert (sel[B - 1][0] >= prefix).all()
+    pick = [int(sel[0][0][k]) for k in (1, 300, 600)]
+    assert all(j < prefix for j in pick)
+    channel = (5, d - 1, 0)
+    for j, ch, v in zip(pick, channel, (1.0, -1.0, 1.0)):
+        c.V[c.table[0, j // 64].long(), 0, j % 64, ch] = v * float("inf")
+    got = c.run(want[0])
+    assert torch.equal(got[1][B - 1], want[1][B - 1]) and torch.equal(got[2], want[2])
+    for s in range(B - 1):
+        other = torch.ones(d, dtype=torch.bool, device="cuda")
+        for j, ch, v in zip(pick, channel, (1.0, -1.0, 1.0)):
+            if j in sel[s][0]:
+                assert got[1][s, 0, ch] == v * float("inf")
+                other[ch] = False
+        assert (got[1][s, 0, other].float() - want[1][s, 0, other].float()).abs().max() <= 2.0 ** -8 * 4
+    for s in range(B):
+        c.K[c.table[s, :20].long()] = float("nan")
+    got = c.run(want[0])
+    assert torch.equal(got[1][B - 1], want[1][B - 1]) and torch.equal(got[2][B - 1], want[2][B - 1])
+    assert torch.isnan(got[1][:B - 1].float()).all() and torch.isnan(got[2][:B - 1]).all()
 
 
 def test_shared_prefix_bad_pages_and_short_lengths():

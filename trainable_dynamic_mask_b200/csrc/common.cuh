@@ -138,6 +138,8 @@ inline cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int block,
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
+// e^(x - m)
+DMA_DEVINL float exp_diff(float x, float m) { return fast_exp2((x - m) * kLog2e); }
 constexpr float kLn2 = 0.6931471805599453f;
 
 }  // namespace dma

@@ -130,6 +130,7 @@ struct PagedPlan {
   int B, H, Hkv, d, w, N, G;
   float scale;
   bool bf16, shared;        // shared: the prefix is selected from and attended to once for the batch
+  bool cand_tc;             // shared: by the tcgen05 kernel
   const int32_t* w_heads;
   char* K;
   char* V;
@@ -141,7 +142,7 @@ struct PagedPlan {
   int cand_len;             // shared: candidates of the prefix per head, min(w, prefix)
   int n_split;              // partial results of a row's list
   int n_psplit;             // shared: partial results of the candidates
-  int cand_split;           // shared: candidates of a CTA (64, 128 or 256)
+  int cand_split;           // shared: candidates of a CTA (64 to 512)
   size_t off_status, off_rows, off_sel, off_cand;
   size_t off_ent;           // int2 [B*H, sel_len]: {slot of the cache, delta bits} beside off_sel
   size_t off_crow;          // int32 [H]: candidates of the head (-1: a bad page among the prefix's)
@@ -163,6 +164,7 @@ struct PagedAppendArgs {
 };
 cudaError_t launch_paged_append(const PagedPlan& P, const PagedAppendArgs& a, void* ws, cudaStream_t s);
 cudaError_t launch_paged_topk(const PagedPlan& P, void* ws, cudaStream_t s);
+cudaError_t launch_paged_cand_tc(const PagedPlan& P, const void* Q, void* ws, cudaStream_t s);
 cudaError_t launch_paged_attn(const PagedPlan& P, const void* Q, void* ws, void* O, float* LSE, cudaStream_t s);
 
 // ---------------------------------------------------------------- launchers (cudaError_t)

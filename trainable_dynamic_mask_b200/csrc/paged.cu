@@ -42,11 +42,23 @@ dma_status_t paged_plan(const dma_params_t* p, const dma_pages_t* c, PagedPlan* 
   if (P->sel_len < 1) P->sel_len = 1;
   P->cand_len = P->shared ? (P->w < P->prefix ? P->w : P->prefix) : 0;
   P->n_split = (P->sel_len + kPagedSplit - 1) / kPagedSplit;
-  // candidates of a CTA: 256, or as few as 64 where that leaves SMs without one (a fixed count of 148
-  // keeps the workspace's plan independent of the device)
-  P->cand_split = 256;
+  // Candidates: the tcgen05 kernel (64 sequences a CTA, one CTA an SM) where every SM has 128 or more of them to
+  // work on, else the smaller CTAs of paged_attn.cu.  Attention over 2048 candidates of 32 heads, 64 sequences:
+  // 31.4 us against 42.3 (33.4 with 64 sequences a CTA there too); 1024 of 16 heads, 128 sequences: 26.3 against
+  // 29.5; but 512 of 16 heads, 48 sequences: 19.1 against 16.4, 100 of 32 heads, 40 sequences: 17.4 against 15.6.
+  // (a fixed count of 148 SMs keeps the workspace's plan independent of the device)
   const int64_t tiles = (int64_t)P->H * ((P->B + 63) / 64);
-  while (P->cand_split > 64 && tiles * ((P->cand_len + P->cand_split - 1) / P->cand_split) < 148) P->cand_split /= 2;
+  P->cand_tc = P->shared && P->B > 32 && tiles * P->cand_len >= 148 * 128;
+  if (P->cand_tc) {
+    // 512 candidates a CTA, or 256 where that takes less than 4/3 as many rounds
+    auto rounds = [&](int split) { return (tiles * ((P->cand_len + split - 1) / split) + 147) / 148; };
+    P->cand_split = 3 * rounds(256) < 4 * rounds(512) ? 256 : 512;
+  } else {
+    // 256, or as few as 64 where that leaves SMs without one
+    P->cand_split = 256;
+    const int64_t small = (int64_t)P->H * ((P->B + 31) / 32);
+    while (P->cand_split > 64 && small * ((P->cand_len + P->cand_split - 1) / P->cand_split) < 148) P->cand_split /= 2;
+  }
   P->n_psplit = (P->cand_len + P->cand_split - 1) / P->cand_split;
   const size_t BH = (size_t)P->B * P->H;
   size_t off = 0;

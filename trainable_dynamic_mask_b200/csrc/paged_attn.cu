@@ -10,8 +10,9 @@
 // memory.  Every lane reads back just what it copied itself, so nothing waits for another warp before the
 // end.  Each group keeps its own running maximum and sum; they meet once per CTA.
 // paged_cand_kernel (shared prefix) multiplies all sequences' queries of a head with the head's
-// candidates: 16 x 64 score tiles on the tensor cores, a sequence's selection being a comparison of the
-// candidate's delta with the edge of its row.
+// candidates, a sequence's selection being a comparison of the candidate's delta with the edge of its row.
+// Few sequences or few candidates give the tensor cores little to do and CTAs of 128 rows little to share:
+// 16 x 64 score tiles of warp-level products; the others go to paged_cand_tc.cu.
 // The partial results (m, l, o) of a row are joined, in a fixed order, by the CTA of its list that
 // finishes last.
 #include <utility>
@@ -20,8 +21,6 @@
 
 namespace dma {
 namespace {
-
-DMA_DEVINL float exp_diff(float x, float m) { return fast_exp2((x - m) * kLog2e); }
 
 // A slot of the cache; what the selection wrote always is one, a workspace it has not been run on may hold
 // anything, which must not be followed.
@@ -253,7 +252,7 @@ paged_list_kernel(const T* __restrict__ Q, const T* __restrict__ K, const T* __r
 constexpr int kPcTile = 64;    // candidates of a pipeline stage
 constexpr int kPcMost = 256;   // candidates of a CTA at most
 
-template <int D> constexpr int cand_smem() { return (64 + 4 * kPcTile) * D * 2; }   // Q, 2 x (K, V)
+template <int D> constexpr int cand_smem() { return (32 + 4 * kPcTile) * D * 2; }   // Q, 2 x (K, V)
 
 // ldmatrix (and its transposing form) at a constant offset from a lane's address.
 template <int OFF> DMA_DEVINL void ldm4(uint32_t at, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
@@ -272,10 +271,8 @@ template <int... I, typename F> DMA_DEVINL void each_of(std::integer_sequence<in
 }
 template <int N, typename F> DMA_DEVINL void each(F f) { each_of(std::make_integer_sequence<int, N>(), f); }
 
-// CTA = (part of a head's candidates, head, 16 R sequences).  Its warps (eight, four for R = 1) are R groups
-// of 16 sequences times 2 or 4 groups of keys: with four warps of a group to a tile, a warp's products and
-// exponentials are what a tile takes.  Tiles of 64 candidates' K and V rows
-// are gathered with 16-byte asynchronous copies (swizzled by row, conflict-free for ldmatrix), one tile
+// CTA = (part of a head's candidates, head, 16 R sequences), R = 1 or 2.  Its 4 R warps are R groups of 16
+// sequences times 4 groups of keys.  Tiles of 64 candidates' K and V rows are gathered with 16-byte asynchronous copies (swizzled by row, conflict-free for ldmatrix), one tile
 // ahead.  A weight is split into two bf16 parts, both multiplied with V: one part alone would round every
 // weight to 8 bits, as much as the output's own rounding.
 // A candidate that a sequence did not select has weight exactly 0 there; if its V row holds an infinity or
@@ -293,7 +290,7 @@ paged_cand_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ K
   constexpr int CH = D / 8, KG = kPcWarps / R, NT = 8 / KG, NO = D / 8;   // NT, NO: 8-wide tiles of keys, channels
   extern __shared__ __align__(128) unsigned char csm[];
   uint16_t* Qs = reinterpret_cast<uint16_t*>(csm);   // [16 R][D]
-  uint16_t* Ks = Qs + 64 * D;                        // [2][64][D]
+  uint16_t* Ks = Qs + 32 * D;                        // [2][64][D]
   uint16_t* Vs = Ks + 2 * kPcTile * D;               // [2][64][D]
   __shared__ __align__(8) uint32_t ckey[kPcMost];
   __shared__ __align__(8) float cdel[kPcMost];
@@ -544,9 +541,8 @@ cudaError_t launch_cand(const PagedPlan& P, const void* Q, void* ws, cudaStream_
 
 template <int D>
 cudaError_t launch_cand_rows(const PagedPlan& P, const void* Q, void* ws, cudaStream_t s) {
-  if (P.B <= 16) return launch_cand<D, 1>(P, Q, ws, s);
-  if (P.B <= 32) return launch_cand<D, 2>(P, Q, ws, s);
-  return launch_cand<D, 4>(P, Q, ws, s);
+  if (P.cand_tc) return launch_paged_cand_tc(P, Q, ws, s);
+  return P.B <= 16 ? launch_cand<D, 1>(P, Q, ws, s) : launch_cand<D, 2>(P, Q, ws, s);
 }
 
 template <typename T, int D, int NT>
