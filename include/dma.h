@@ -23,11 +23,13 @@
  *    dma_gate_bwd_noalloc.  Calls on different streams may run concurrently when their buffers
  *    (including workspaces) are distinct; dma_gate_bwd_noalloc calls must not overlap.
  *  - All pointers are device pointers, 16-byte aligned, to dense row-major (C-contiguous)
- *    tensors with the layouts given per argument.  The caller owns every buffer.
+ *    tensors with the layouts given per argument (dma_prep, dma_prep_bwd and dma_paged_append also
+ *    take projections at strides).  The caller owns every buffer.
  *  - Arguments are validated before anything is launched.  On any error nothing is launched
  *    and no output is touched, except DMA_ERR_CUDA, which reports a failed launch (outputs are
  *    then unspecified).
- *  - Outputs are fully overwritten, never accumulated into.
+ *  - Outputs are fully overwritten, never accumulated into (dma_paged_append and the strided gradients
+ *    of dma_prep_bwd write the rows they are asked for and leave the rest of their tensors as it is).
  *  - Tensor names follow the page: Q, K, V, Delta (the sampling weights), A (per-head
  *    selective control), delta (the dynamic weights), O, LSE.
  *
@@ -359,7 +361,7 @@ dma_status_t dma_cp_compact(const dma_params_t* p, int32_t prefix_len, int32_t n
  *   (a, b) -> (a cos - b sin, b cos + a sin), the pair being channels (i, i + rot/2), or
  *   (2i, 2i + 1) when `interleaved` is 1.  Angles are formed in double precision and every result is
  *   rounded once.  Value rows are copied.
- * Position n of row (b, i): positions[b * N + i] where given, else first + i.
+ * Position n of row (b, i): positions[b * N + i] where given, else first + i (which must fit int32).
  *   rot       0 .. d, a multiple of 16; inv_freq (float32 [rot/2], radians per position) NULL iff rot == 0
  *   eps       finite, > 0
  */
@@ -384,7 +386,8 @@ typedef struct {
 /*
  * Forward.  q, k, v: strided as st says (H, Hkv, Hkv heads of d channels, dtype).  Out: Q [B, H, N, d],
  * K, V [B, Hkv, N, d] dtype, dense.  v and V may be NULL together.  p: B, H, Hkv, N, d and dtype are
- * used, Nq must equal N; N <= 2^24, B N < 2^31 (no other limit of the attention applies).  Outputs must not overlap inputs.
+ * used, Nq must equal N; N <= 2^24, B N < 2^31 (of the attention's other limits d in {64, 128} and
+ * B H <= 65535 apply).  Outputs must not overlap inputs.
  */
 dma_status_t dma_prep(const dma_params_t* p, const dma_prep_t* r, const dma_prep_strides_t* st, const void* q,
                       const void* k, const void* v, void* Q, void* K, void* V, void* stream);
@@ -400,7 +403,7 @@ dma_status_t dma_prep_workspace_size(const dma_params_t* p, const dma_prep_t* r,
  * Out: dq, dk, dv, strided as gst says, dtype (rows must not overlap one another: DMA_ERR_INVALID_ARG);
  * what lies between the rows is left as it is.  dV and dv may be NULL together (dV_gate too, then).
  * dq_weight, dk_weight [d] float32, sums over every row; each may be NULL, and must be where the weight
- * is.  The sums do not depend on scheduling: two runs give the same bits.
+ * is.  Outputs must not overlap inputs.  The sums do not depend on scheduling: two runs give the same bits.
  */
 dma_status_t dma_prep_bwd(const dma_params_t* p, const dma_prep_t* r, const dma_prep_strides_t* st,
                           const dma_prep_strides_t* gst, const void* q, const void* k, const void* dQ,

@@ -50,6 +50,8 @@ def _pages(**kw):
     (dict(interleaved=2), INVALID),
     (dict(q_weight=FAKE + 4), INVALID),
     (dict(positions=FAKE + 8), INVALID),
+    (dict(positions=None, first=2**31 - 256), OK),
+    (dict(positions=None, first=2**31 - 255), INVALID),   # the last position would not be an int32
 ])
 def test_prep_description(kw, expect):
     p = dma.make_params(1, 2, 1, 256, 64, 1)

@@ -65,6 +65,9 @@ template <int D, int V> DMA_DEVINL void join(const float* part, int n, int c, fl
   m = big;
 }
 
+// Three stages on their way of 4 keys a group (K and V: 48 KB of a CTA of 128 threads, four of which share an
+// SM).  2048 keys for each of 256 queries, 268 MB of 256-byte rows anywhere in 2 GB, take 50 us (5.3 TB/s, 81 % of the
+// copy rate); with two stages or four 1 us more.
 constexpr int kPlStages = 3;
 
 template <typename T> constexpr int list_keys() { return sizeof(T) == 2 ? 4 : 2; }   // keys of a group and stage
@@ -558,7 +561,7 @@ cudaError_t launch_list_t(const PagedPlan& P, const void* Q, void* ws, void* O, 
 template <typename T, int D>
 cudaError_t launch_list(const PagedPlan& P, const void* Q, void* ws, void* O, float* LSE, cudaStream_t s) {
   // behind a shared prefix a row lists about w (N - prefix) / N keys; one warp is enough for few of them, if
-  // there are rows enough to fill the GPU with such CTAs
+  // there are rows enough to fill the GPU with such CTAs: 2048 rows of some 15 keys 9.5 us, with 128 threads 17.7
   if (P.shared && P.B * P.H >= 8 * sm_count() && (int64_t)P.w * (P.N - P.prefix) <= (int64_t)64 * P.N)
     return launch_list_t<T, D, 32>(P, Q, ws, O, LSE, s);
   return launch_list_t<T, D, 128>(P, Q, ws, O, LSE, s);
