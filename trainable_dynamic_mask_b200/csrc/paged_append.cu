@@ -12,7 +12,8 @@
 // would take 4 us less, the gate alone 9.  What is left is a short call's: a plain copy of as many bytes
 // stays a third below its rate for long ones.  Two CTAs an SM with four chunks on their way took 28.6 us,
 // three with four 27.5, four (64 registers) 29; the gate's CTAs first, or with four stages, the same.
-// One token of a sequence (8 rows) takes 5 us, bound by latency: the lookup's reads, one wave of rows, the gate.
+// One token for each of 8 sequences takes 8.5 us in a graph, bound by latency: the lookup's reads, one wave of
+// rows, the gate (3 us of it).
 #include "rows.cuh"
 
 namespace dma {

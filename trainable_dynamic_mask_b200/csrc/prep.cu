@@ -12,8 +12,8 @@
 // else moves.  16384 tokens of 16 + 8 + 8 heads of 128 channels in bf16: forward 268 MB in 52 us (5.1 TB/s, 78 %
 // of the copy rate of 6.56), backward 436 MB in 90 us (4.9 TB/s, 74 %); the rest is issue slots (71 % of them
 // in the forward).  Forward with three CTAs an SM 53 us, with two 57; backward with two 92, with one 118.
-// Small calls are bound by the way through the binding and the launch: 8 tokens in 8.4 us, of which the
-// kernel 4 (the backward has a second launch, of the weights' sums, that starts while the first ends).
+// Small calls are bound by the way through the binding and the launch: 8 tokens in 8.4 us, 5 in a
+// graph (the backward has a second launch, of the weights' sums, that starts while the first ends).
 #include <math.h>
 #include <string.h>
 
