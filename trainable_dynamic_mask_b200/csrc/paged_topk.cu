@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : NT == 256 ? 4 : 8)
 paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict__ sel, int2* __restrict__ ent,
                     int32_t* __restrict__ crow, int32_t* __restrict__ cand, int2* __restrict__ cent,
                     int2* __restrict__ tail, int32_t* __restrict__ counters, int32_t* __restrict__ status, int cap, int page_cap,
-                    int list_cap) {
+                    int list_cap, bool longest_first) {
   constexpr int NW = NT / 32, BINS = 4 * NT, LB = NT == 512 ? 11 : NT == 256 ? 10 : 9;
   static_assert(BINS == 1 << LB, "four counters a thread");
   static_assert(!SIEVE || M == kRows, "candidates and their rest are short or few");
@@ -193,10 +193,31 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
   };
   // p in the shared memory of CTA r of the cluster
   auto of = [&](auto* p, int r) { return CL ? cl.map_shared_rank(p, r) : p; };
-  const int row = blockIdx.y, h = M == kCandidates ? row : row % P.H, b = M == kCandidates ? 0 : row / P.H;
+  const int h = M == kCandidates ? blockIdx.y : blockIdx.y % P.H;
+  int b = M == kCandidates ? 0 : blockIdx.y / P.H;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
   pdl_wait();
+  if (M == kRows && longest_first) {
+    // this CTA's sequence: the one of that place in the order of lengths, the longest first
+    __shared__ int place;
+    const int want = b;
+    if (tid == 0) place = want;
+    __syncthreads();
+    for (int t = tid; t < P.B; t += NT) {
+      const int n = __ldg(P.lens + t);
+      int before = 0;
+#pragma unroll 8
+      for (int u = 0; u < P.B; ++u) {
+        const int o = __ldg(P.lens + u);
+        before += o > n || (o == n && u < t);
+      }
+      if (before == want) place = t;
+    }
+    __syncthreads();
+    b = place;
+  }
+  const int row = M == kCandidates ? h : b * P.H + h;
   const int W = row_window(P.w_heads, h, P.H, P.w);
   const int page = 1 << P.page_shift;
   const int32_t* tab = P.table + (size_t)b * P.max_pages;
@@ -896,7 +917,8 @@ cudaError_t launch_select_t(const PagedPlan& P, int n_rows, int n, int C, int ca
   const cudaError_t e = ensure_smem_limit(paged_select_kernel<M, NT, SIEVE, CL>, (int)smem);
   if (e != cudaSuccess) return e;
   return launch_after(paged_select_kernel<M, NT, SIEVE, CL>, dim3(C, n_rows), NT, smem, s, CL ? C : 1,
-                      P, ws_ptr<int32_t>(ws, P.off_rows), ws_ptr<int32_t>(ws, P.off_sel), ws_ptr<int2>(ws, P.off_ent), ws_ptr<int32_t>(ws, P.off_crow), ws_ptr<int32_t>(ws, P.off_cand), ws_ptr<int2>(ws, P.off_cent), ws_ptr<int2>(ws, P.off_tail), ws_ptr<int32_t>(ws, P.off_count), ws_ptr<int32_t>(ws, P.off_status), cap, page_cap, list_cap);
+                      P, ws_ptr<int32_t>(ws, P.off_rows), ws_ptr<int32_t>(ws, P.off_sel), ws_ptr<int2>(ws, P.off_ent), ws_ptr<int32_t>(ws, P.off_crow), ws_ptr<int32_t>(ws, P.off_cand), ws_ptr<int2>(ws, P.off_cent), ws_ptr<int2>(ws, P.off_tail), ws_ptr<int32_t>(ws, P.off_count), ws_ptr<int32_t>(ws, P.off_status), cap, page_cap, list_cap,
+                      M == kRows && P.B > 1 && P.B <= 256 && n_rows * NT > sm_count() * 1024);
 }
 
 // Launches the selection of `n_rows` rows of at most n values.
