@@ -680,6 +680,50 @@ def test_two_streams_and_graphs_that_share_a_workspace():
         assert torch.equal(x, y)
 
 
+def test_large_shared_batch_in_a_graph_beside_another_stream():
+    """The tcgen05 kernel captured and replayed as lengths change, while the same call runs on another stream."""
+    prefix = 1280
+    c = Cache([prefix + 1 + i % 20 for i in range(40)], 16, 4, 64, 64, "bf16", 1200, seed=5, prefix=prefix, N=prefix + 64)
+    torch, dma = c.torch, c.dma
+    Q, O, L = c.run()
+    full = [x.clone() for x in (O, L)]
+    lens = c.lens.clone()
+    side, ws2 = torch.cuda.Stream(), dma.alloc_paged_workspace(c.p, c.c)
+    O2, L2 = torch.empty_like(O), torch.empty_like(L)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        dma.paged_topk(c.p, c.c, c.ws)
+        dma.paged_attn(c.p, c.c, Q, c.ws, O, L)
+    for grow in (30, 0, 7):
+        c.lens.copy_(lens + grow)
+        c.lens[3] = 0
+        torch.cuda.synchronize()
+        O.fill_(float("nan"))
+        L.fill_(float("nan"))
+        side.wait_stream(torch.cuda.current_stream())
+        graph.replay()
+        with torch.cuda.stream(side):
+            dma.paged_topk(c.p, c.c, ws2)
+            dma.paged_attn(c.p, c.c, Q, ws2, O2, L2)
+        torch.cuda.synchronize()
+        assert torch.equal(O, O2) and torch.equal(L, L2)
+        assert (O[3] == 0).all() and (L[3] == -float("inf")).all()
+        if grow == 0:
+            keep = torch.arange(40, device="cuda") != 3
+            assert torch.equal(O[keep], full[0][keep]) and torch.equal(L[keep], full[1][keep])
+    assert dma.check_device_status(c.p, c.ws) == 0
+
+
+def test_many_rows_of_any_lengths():
+    """Rows that take several rounds are taken in the order of lengths, equal ones and idle ones among them."""
+    lens = [(i * 977) % 4300 for i in range(60)] + [0, 0, 4300, 4300, 1, 1, 2]
+    c = Cache(lens, 12, 4, 64, 16, "bf16", 40, seed=6)
+    c.dma.paged_topk(c.p, c.c, c.ws)
+    c.torch.cuda.synchronize()
+    c.check_selection()
+
+
 def test_calls_that_the_binding_refuses():
     c = Cache([40, 7], 4, 2, 64, 16, "bf16", 8, seed=50)
     dma, torch = c.dma, c.torch

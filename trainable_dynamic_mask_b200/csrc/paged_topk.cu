@@ -26,7 +26,8 @@
 // values, counters, the edge's interval, the list), each a wait of a microsecond, and the instructions of the
 // rows that share an SM (58 % of the issue slots for 768 rows of up to 8192 values).  Measured: 8 sequences of
 // 65536 values, 32 heads, window 2048 (67 MB): 36 us, of which the first reading 13.5 (5 TB/s); without the
-// sieve 95.  48 sequences of up to 8192 values, 16 heads (12.6 MB): 26 us.  A prefix of 32768 values, 32 heads:
+// sieve 95.  48 sequences of up to 8192 values, 16 heads (12.6 MB): 25 us
+// (27 before the longest came first).  A prefix of 32768 values, 32 heads:
 // candidates 18.5 us, 64 sequences' own keys behind it 9 (25 more without rest_by_tail).
 #include <cooperative_groups.h>
 
@@ -945,8 +946,8 @@ cudaError_t launch_select(const PagedPlan& P, int n_rows, int n, void* ws, cudaS
   // clusters: stretches of at most 16384 values, and for few rows as many CTAs as there are SMs for (more
   // would wait: a cluster needs its SMs side by side), down to stretches of 2048 (32 rows of 32768 values in
   // four stretches rather than two: 18.5 us against 22); short rows in large numbers go to small CTAs, more of
-  // which share an SM: 768 rows of up to 8192 values with 256 threads 28.7 us, with 512 32.8 (with 128, or
-  // five CTAs of 256 an SM, the same); 2048 rows of some 2300 with 128 threads 9 us, with 512 25
+  // which share an SM: 768 rows of up to 8192 values with 256 threads 25.9 us, with 512 30.7 (with 128, or
+  // five CTAs of 256 an SM, 28); 2048 rows of some 2300 with 128 threads 9 us, with 512 25
   int C = 1;
   while (C < kPsMaxCluster && ((n + C - 1) / C > 16384 || (2 * n_rows * C <= sms && (n + C - 1) / C > 2048))) C *= 2;
   const int seg = ((n + C - 1) / C + 3) & ~3, cap = seg + 4 < 40960 ? seg + 4 : 40960;
