@@ -24,11 +24,14 @@
 //
 // The bytes are one reading of the gate values; what bounds a row is the chain of its steps (page numbers,
 // values, counters, the edge's interval, the list), each a wait of a microsecond, and the instructions of the
-// rows that share an SM (58 % of the issue slots for 768 rows of up to 8192 values).  Measured: 8 sequences of
+// rows that share an SM (58 % of the issue slots for 768 rows of up to 8192 values).  A CTA passes through
+// most of its code once, so instructions that have to come from memory first are a part of that chain: loops
+// over the resident keys are not unrolled and clusters of up to 4 have a kernel of their own, which takes 4 us
+// off a selection of 20 (8 sequences behind a prefix of 2048).  Measured: 8 sequences of
 // 65536 values, 32 heads, window 2048 (67 MB): 36 us, of which the first reading 13.5 (5 TB/s); without the
 // sieve 95.  48 sequences of up to 8192 values, 16 heads (12.6 MB): 25 us
 // (27 before the longest came first).  A prefix of 32768 values, 32 heads:
-// candidates 18.5 us, 64 sequences' own keys behind it 9 (25 more without rest_by_tail).
+// candidates 17 us, 64 sequences' own keys behind it 8 (25 more without rest_by_tail).
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -163,8 +166,8 @@ DMA_DEVINL bool rest_by_tail(const PagedPlan& P, const int32_t* tab, int h, int 
   return true;
 }
 
-// CL: clusters of more than one CTA.
-template <SelMode M, int NT, bool SIEVE, bool CL>
+// MC: CTAs of a cluster at most.
+template <SelMode M, int NT, bool SIEVE, int MC>
 __global__ void __launch_bounds__(NT, NT == 512 ? 2 : NT == 256 ? 4 : 8)
 paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict__ sel, int2* __restrict__ ent,
                     int32_t* __restrict__ crow, int32_t* __restrict__ cand, int2* __restrict__ cent,
@@ -186,7 +189,8 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
   __shared__ int found_bin, found_above, found_count, other_bin, other_above;
   __shared__ uint32_t found_key;
   cg::cluster_group cl = cg::this_cluster();
-  constexpr int kMost = CL ? kPsMaxCluster : 1;
+  constexpr int kMost = MC;
+  constexpr bool CL = MC > 1;
   const int C = CL ? (int)cl.num_blocks() : 1, rank = CL ? (int)cl.block_rank() : 0;
   auto all_sync = [&]() {
     if (CL) cl.sync();
@@ -312,7 +316,7 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
   };
   // fn(key) for every key of the stretch, in no particular order
   auto for_keys = [&](auto fn) {
-#pragma unroll 4
+#pragma unroll 1
     for (int i = tid * 4; i < res; i += NT * 4) {
       const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
       fn(k.x); fn(k.y); fn(k.z); fn(k.w);
@@ -432,6 +436,7 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
       if (i + 3 >= ns) f.w = nothing;
       return f;
     };
+    static_assert(kU * 128 == 1024, "a warp's chunk below: every maximum of it is written");
     float fmin = INFINITY, fmax = -INFINITY;
     for (int c0 = warp * 1024; c0 < ns; c0 += NW * 1024) {   // 1024 neighbouring keys of a warp
       float4 f[kU];
@@ -672,6 +677,7 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
         if (tid < m) {
           const uint32_t k = every[tid];
           int gt = above, ge = above;
+#pragma unroll 2
           for (int i = 0; i < m; ++i) {
             const uint32_t o = every[i];
             gt += o > k;
@@ -732,7 +738,7 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
     if (tid == 0) cnt[2] = wx.y, cnt[3] = wy.y;   // the CTA's, for the sums over the cluster
   } else if (!bad) {
     auto count = [&](auto resident) {
-#pragma unroll 4
+#pragma unroll 1
       for (int j = j0 + lane * 4; j < j1; j += 128) {
         const uint4 k4 = resident || j < cap ? *reinterpret_cast<const uint4*>(keys + j) : load4(i0 + j);
         const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
@@ -908,16 +914,16 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
 }
 
 // cap: words of shared memory for keys.
-template <SelMode M, int NT, bool SIEVE, bool CL>
+template <SelMode M, int NT, bool SIEVE, int MC>
 cudaError_t launch_select_t(const PagedPlan& P, int n_rows, int n, int C, int cap, int list_cap, void* ws,
                             cudaStream_t s) {
   const int seg = ((n + C - 1) / C + 3) & ~3;
   int page_cap = (seg >> P.page_shift) + 2;
   if (page_cap > 4100) page_cap = 4100;   // 65536 positions in the smallest pages
   const size_t smem = (size_t)(cap + page_cap) * 4;
-  const cudaError_t e = ensure_smem_limit(paged_select_kernel<M, NT, SIEVE, CL>, (int)smem);
+  const cudaError_t e = ensure_smem_limit(paged_select_kernel<M, NT, SIEVE, MC>, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_after(paged_select_kernel<M, NT, SIEVE, CL>, dim3(C, n_rows), NT, smem, s, CL ? C : 1,
+  return launch_after(paged_select_kernel<M, NT, SIEVE, MC>, dim3(C, n_rows), NT, smem, s, MC > 1 ? C : 1,
                       P, ws_ptr<int32_t>(ws, P.off_rows), ws_ptr<int32_t>(ws, P.off_sel), ws_ptr<int2>(ws, P.off_ent), ws_ptr<int32_t>(ws, P.off_crow), ws_ptr<int32_t>(ws, P.off_cand), ws_ptr<int2>(ws, P.off_cent), ws_ptr<int2>(ws, P.off_tail), ws_ptr<int32_t>(ws, P.off_count), ws_ptr<int32_t>(ws, P.off_status), cap, page_cap, list_cap,
                       M == kRows && P.B > 1 && P.B <= 256 && n_rows * NT > sm_count() * 1024);
 }
@@ -939,8 +945,8 @@ cudaError_t launch_select(const PagedPlan& P, int n_rows, int n, void* ws, cudaS
       list_cap = (list_cap + 7) & ~7;
       const int cap = 2 * list_cap + list_cap / 2;
       if (seg <= 65536 && list_cap <= 32 * kPsMaxBatches && cap <= 36864)
-        return C > 1 ? launch_select_t<M, 512, true, true>(P, n_rows, n, C, cap, list_cap, ws, s)
-                     : launch_select_t<M, 512, true, false>(P, n_rows, n, C, cap, list_cap, ws, s);
+        return C > 1 ? launch_select_t<M, 512, true, kPsMaxCluster>(P, n_rows, n, C, cap, list_cap, ws, s)
+                     : launch_select_t<M, 512, true, 1>(P, n_rows, n, C, cap, list_cap, ws, s);
     }
   }
   // clusters: stretches of at most 16384 values, and for few rows as many CTAs as there are SMs for (more
@@ -951,12 +957,13 @@ cudaError_t launch_select(const PagedPlan& P, int n_rows, int n, void* ws, cudaS
   int C = 1;
   while (C < kPsMaxCluster && ((n + C - 1) / C > 16384 || (2 * n_rows * C <= sms && (n + C - 1) / C > 2048))) C *= 2;
   const int seg = ((n + C - 1) / C + 3) & ~3, cap = seg + 4 < 40960 ? seg + 4 : 40960;
-  if (C > 1) return launch_select_t<M, 512, false, true>(P, n_rows, n, C, cap, 0, ws, s);
+  if (C > 4) return launch_select_t<M, 512, false, kPsMaxCluster>(P, n_rows, n, C, cap, 0, ws, s);
+  if (C > 1) return launch_select_t<M, 512, false, 4>(P, n_rows, n, C, cap, 0, ws, s);
   if (n_rows >= 4 * sms) {
-    if (seg <= 4096) return launch_select_t<M, 128, false, false>(P, n_rows, n, C, cap, 0, ws, s);
-    if (seg <= 8192) return launch_select_t<M, 256, false, false>(P, n_rows, n, C, cap, 0, ws, s);
+    if (seg <= 4096) return launch_select_t<M, 128, false, 1>(P, n_rows, n, C, cap, 0, ws, s);
+    if (seg <= 8192) return launch_select_t<M, 256, false, 1>(P, n_rows, n, C, cap, 0, ws, s);
   }
-  return launch_select_t<M, 512, false, false>(P, n_rows, n, C, cap, 0, ws, s);
+  return launch_select_t<M, 512, false, 1>(P, n_rows, n, C, cap, 0, ws, s);
 }
 
 }  // namespace
