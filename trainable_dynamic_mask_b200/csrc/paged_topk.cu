@@ -951,7 +951,7 @@ cudaError_t launch_select(const PagedPlan& P, int n_rows, int n, void* ws, cudaS
   }
   // clusters: stretches of at most 16384 values, and for few rows as many CTAs as there are SMs for (more
   // would wait: a cluster needs its SMs side by side), down to stretches of 2048 (32 rows of 32768 values in
-  // four stretches rather than two: 18.5 us against 22); short rows in large numbers go to small CTAs, more of
+  // four stretches rather than two: a sixth less time); short rows in large numbers go to small CTAs, more of
   // which share an SM: 768 rows of up to 8192 values with 256 threads 25.9 us, with 512 30.7 (with 128, or
   // five CTAs of 256 an SM, 28); 2048 rows of some 2300 with 128 threads 9 us, with 512 25
   int C = 1;
