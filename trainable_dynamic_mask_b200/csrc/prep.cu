@@ -9,7 +9,7 @@
 // and dv = dV + dV_gate.  r is formed again from x, which the norm's gradient reads anyway.
 //
 // Both are bound by memory where there are many rows: every row is read once and written once, and nothing
-// else moves.  16384 tokens of 16 + 8 + 8 heads of 128 channels in bf16: forward 268 MB in 52 us (5.1 TB/s, 78 %
+// else moves.  16384 tokens of 16 + 8 + 8 heads of 128 channels in bf16: forward 268 MB in 51 us (5.2 TB/s, 80 %
 // of the copy rate of 6.56), backward 436 MB in 90 us (4.9 TB/s, 74 %); the rest is issue slots (71 % of them
 // in the forward).  Forward with three CTAs an SM 53 us, with two 57; backward with two 92, with one 118.
 // Small calls are bound by the way through the binding and the launch: 8 tokens in 8.4 us, 5 in a
@@ -24,7 +24,7 @@ namespace {
 
 // Dense outputs [B, heads, N, D].
 struct DenseDest {
-  static constexpr int kDepth = 4;
+  static constexpr int kDepth = 3;   // with two or four 0.2 and 1 us more at 16384 tokens
   struct Token {
     int position;
     unsigned b, n;
