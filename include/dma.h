@@ -470,8 +470,10 @@ dma_status_t dma_paged_layout(const dma_params_t* p, const dma_pages_t* c, dma_p
  *   q, k, v  strided {-, token, head} as st says (H, Hkv, Hkv heads), dtype;  Q [T, H, d] dtype, dense.  q and
  *            Q may be NULL together.  Rows of padding, idle rows and skipped tokens are left as they were.
  *   Delta [Hkv*d, H] dtype, A [H] float32
- * No two sequences may append to the same slot.  x is accumulated in float32.  The call is complete in the
- * stream's order like any other; it needs the workspace for its status word only.
+ * No two sequences may append to the same slot.  A shared prefix is therefore written by one sequence, whose
+ * length reaches it, or before it is described as one (with prefix 0): tokens of a sequence shorter than the
+ * prefix are skipped and reported.  x is accumulated in float32.  The call is complete in the stream's order
+ * like any other; it needs the workspace for its status word only.
  */
 dma_status_t dma_paged_append(const dma_params_t* p, const dma_pages_t* c, const dma_prep_t* r,
                               const dma_prep_strides_t* st, int32_t T, const int32_t* starts, const void* q,

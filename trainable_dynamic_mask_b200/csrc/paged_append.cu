@@ -70,8 +70,9 @@ DMA_DEVINL Place place_of(const PagedPlan& P, const PagedAppendArgs& a, int t, b
   }
   if (!wanted || len <= 0) return {seq, -1, 0, 0};
   const int pos = len - n + (t - first);
-  int page = -1;
-  if (pos >= 0 && pos < len && len <= P.N) page = __ldg(P.table + (size_t)seq * P.max_pages + (pos >> P.page_shift));
+  int page = -1;   // a length below the prefix would lead into the pages that the batch shares
+  if (pos >= 0 && pos < len && len >= P.prefix && len <= P.N)
+    page = __ldg(P.table + (size_t)seq * P.max_pages + (pos >> P.page_shift));
   if (page < 0 || page >= P.n_pages) {
     atomicOr(status, kPagedErr);
     return {seq, -1, 0, 0};
