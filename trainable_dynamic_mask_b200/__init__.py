@@ -316,7 +316,8 @@ def make_pages(p, K, V, delta, table, lens, prefix=0) -> DmaPages:
     """dma_pages_t: the paged cache of p's sequences.  K, V [n_pages, Hkv, page, d], delta
     [n_pages, H, page] float32, table int32 [B, max_pages], lens int32 [B] (device tensors, which the
     result keeps alive; they may be written to between calls).  prefix: leading positions that every
-    sequence shares, a multiple of the page length."""
+    sequence shares, a multiple of the page length.  The calls below take these pages with parameters of the
+    same heads, channels and type, for as many sequences or fewer (the first ones)."""
     if K.dim() != 4 or table.dim() != 2:
         raise ValueError("K must be [n_pages, Hkv, page, d] and table [B, max_pages]")
     tt = _torch()
@@ -329,6 +330,7 @@ def make_pages(p, K, V, delta, table, lens, prefix=0) -> DmaPages:
                  lens=_dense("lens", lens, (p.B,), tt.i32, dev), n_pages=n, page=page,
                  max_pages=table.shape[1], prefix=int(prefix))
     c.tensors, c.device = (K, V, delta, table, lens), dev
+    c.sequences, c.rows = p.B, (p.H, p.Hkv, p.d, p.dtype)
     return c
 
 
@@ -337,9 +339,20 @@ def _same_device(c, dev):
         raise ValueError(f"the pages are on cuda:{c.device}, the current device is cuda:{dev}")
 
 
+def _same_problem(p, c):
+    """p reads pages as they were made: the same heads, channels and type, and no more sequences (the library
+    sees addresses alone)."""
+    if p.B > c.sequences or (p.H, p.Hkv, p.d, p.dtype) != c.rows:
+        raise ValueError(f"the pages were made for B <= {c.sequences} and (H, Hkv, d, dtype) = {c.rows}, not for "
+                         f"B = {p.B} and {(p.H, p.Hkv, p.d, p.dtype)}")
+
+
 def paged_layout(p, c) -> DmaPagedLayout:
+    call = load().dma_paged_layout
+    if hasattr(c, "rows"):   # pages described by hand are their maker's responsibility
+        _same_problem(p, c)
     lay = DmaPagedLayout()
-    check("dma_paged_layout", load().dma_paged_layout(p, c, lay))
+    check("dma_paged_layout", call(p, c, lay))
     return lay
 
 
@@ -352,6 +365,7 @@ def paged_append(p, c, r, q, k, v, Delta, A, Q, workspace, starts=None, stream=N
     dev, t, f = tt.device(), tt.types[p.dtype], tt.f32
     T, H, Hkv, d = k.shape[0], p.H, p.Hkv, p.d
     _same_device(c, dev)
+    _same_problem(p, c)
     _check_prep_tensors(p, r, dev)
     st = DmaPrepStrides()
     check("dma_paged_append", call(
@@ -367,6 +381,7 @@ def paged_topk(p, c, workspace, stream=None):
     call, tt = load().dma_paged_topk, _torch()
     dev = tt.device()
     _same_device(c, dev)
+    _same_problem(p, c)
     check("dma_paged_topk", call(p, c, _workspace(workspace, dev), _nbytes(workspace),
                                                   tt.stream(dev) if stream is None else _stream(stream)))
 
@@ -377,6 +392,7 @@ def paged_attn(p, c, Q, workspace, O, LSE, stream=None):
     dev, t = tt.device(), tt.types[p.dtype]
     shape = (p.B, p.H, p.d)
     _same_device(c, dev)
+    _same_problem(p, c)
     check("dma_paged_attn", call(
         p, c, _dense("Q", Q, shape, t, dev), _workspace(workspace, dev), _nbytes(workspace),
         _dense("O", O, shape, t, dev), _dense("LSE", LSE, (p.B, p.H), tt.f32, dev), tt.stream(dev) if stream is None else _stream(stream)))
