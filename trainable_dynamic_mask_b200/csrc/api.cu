@@ -17,8 +17,6 @@ namespace {
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool ok_ptr(const void* p) { return p != nullptr && aligned16(p); }
 
-dma_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? DMA_OK : DMA_ERR_CUDA; }
-
 // Validates the workspace for plan P.
 dma_status_t check_ws(const Plan& P, const void* ws, size_t ws_bytes) {
   if (ws == nullptr || !aligned16(ws)) return DMA_ERR_WORKSPACE;
@@ -401,10 +399,10 @@ dma_status_t dma_check_device_status(const dma_params_t* p, void* workspace, voi
   if (workspace == nullptr || code == nullptr) return DMA_ERR_INVALID_ARG;
   cudaStream_t s = (cudaStream_t)stream;
   int32_t v = 0;
-  if (cudaMemcpyAsync(&v, ws_ptr<int32_t>(workspace, P.off_status), sizeof(v),
-                      cudaMemcpyDeviceToHost, s) != cudaSuccess)
-    return DMA_ERR_CUDA;
-  if (cudaStreamSynchronize(s) != cudaSuccess) return DMA_ERR_CUDA;
+  st = cuda_status(cudaMemcpyAsync(&v, ws_ptr<int32_t>(workspace, P.off_status), sizeof(v),
+                                   cudaMemcpyDeviceToHost, s));
+  if (st != DMA_OK) return st;
+  if ((st = cuda_status(cudaStreamSynchronize(s))) != DMA_OK) return st;
   *code = v;
   return v == 0 ? DMA_OK : DMA_ERR_TIMEOUT;
 }

@@ -343,13 +343,13 @@ dma_status_t dma_cp_candidates(const dma_params_t* p, int32_t shard_start, const
   cudaStream_t s = (cudaStream_t)stream;
   int32_t* sel = ws_ptr<int32_t>(workspace, L.off_sel);
   cudaError_t e = launch_topw_select_rows(delta, P.B * P.H, P.N, P.w, P.w_heads, P.H, sel, nullptr, P.w, s);
-  if (e != cudaSuccess) return DMA_ERR_CUDA;
+  if (e != cudaSuccess) return cuda_status(e);
   unsigned char* c = static_cast<unsigned char*>(cand);
   cp_pack_kernel<<<dim3(P.B * P.H, (P.w + kCpThreads - 1) / kCpThreads), kCpThreads, 0, s>>>(sel, delta, (const unsigned char*)K, (const unsigned char*)V,
                                                   reinterpret_cast<int32_t*>(c + L.off_pos),
                                                   reinterpret_cast<float*>(c + L.off_delta), c + L.off_k, c + L.off_v,
                                                   P.H, P.G, P.N, P.w, P.w_heads, shard_start, P.d * L.elt);
-  return cudaGetLastError() == cudaSuccess ? DMA_OK : DMA_ERR_CUDA;
+  return cuda_status(cudaGetLastError());
 }
 
 dma_status_t dma_cp_compact(const dma_params_t* p, int32_t prefix_len, int32_t n_prev, const void* cands,
@@ -376,9 +376,9 @@ dma_status_t dma_cp_compact(const dma_params_t* p, int32_t prefix_len, int32_t n
     cp_gather_delta_kernel<<<(unsigned)((n + 255) / 256 < 148 * 8 ? (n + 255) / 256 : 148 * 8), 256, 0, s>>>(
         cb, L.cand_bytes, L.off_delta, dm, P.B * P.H, n_prev, P.w);
     cudaError_t e = launch_topw_select_rows(dm, P.B * P.H, n_prev * P.w, P.w, P.w_heads, P.H, sel2, nullptr, P.w, s);
-    if (e != cudaSuccess) return DMA_ERR_CUDA;
+    if (e != cudaSuccess) return cuda_status(e);
     const size_t smem = (size_t)L.cap * (sizeof(uint64_t) + sizeof(int32_t));
-    if (ensure_smem_limit(cp_union_kernel, (int)smem) != cudaSuccess) return DMA_ERR_CUDA;
+    if ((e = ensure_smem_limit(cp_union_kernel, (int)smem)) != cudaSuccess) return cuda_status(e);
     int64_t* src = ws_ptr<int64_t>(workspace, L.off_src);
     const int64_t n_rows_w = (int64_t)P.B * P.H * P.w;   // entries of one candidate buffer
     cp_union_kernel<<<P.B * P.Hkv, kCpUnionThreads, smem, s>>>(
@@ -395,7 +395,7 @@ dma_status_t dma_cp_compact(const dma_params_t* p, int32_t prefix_len, int32_t n
   cp_own_kernel<<<grid > 0 ? grid : 1, 256, 0, s>>>(delta, (const unsigned char*)K, (const unsigned char*)V, delta_c,
                                                     (unsigned char*)Kc, (unsigned char*)Vc, pos_c, P.B * P.H,
                                                     P.B * P.Hkv, P.N, Pr, Nc, prefix_len, rb);
-  return cudaGetLastError() == cudaSuccess ? DMA_OK : DMA_ERR_CUDA;
+  return cuda_status(cudaGetLastError());
 }
 
 }  // extern "C"

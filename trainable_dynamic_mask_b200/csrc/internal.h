@@ -84,6 +84,14 @@ struct Plan {
 dma_status_t make_plan(const dma_params_t* p, Plan* plan);
 void fwd_schedule(const Plan& P, FwdSchedule* S);
 
+// Status of an entry point whose last CUDA call returned e.  A failure is also taken out of the runtime's
+// record, where the check behind the next call's launch would find it and report it a second time.
+inline dma_status_t cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return DMA_OK;
+  cudaGetLastError();
+  return DMA_ERR_CUDA;
+}
+
 template <typename T> inline T* ws_ptr(void* ws, size_t off) {
   return reinterpret_cast<T*>(reinterpret_cast<char*>(ws) + off);
 }

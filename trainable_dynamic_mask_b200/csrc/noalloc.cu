@@ -123,9 +123,8 @@ extern "C" dma_status_t dma_gate_bwd_noalloc(const dma_params_t* p, const void* 
   Q.off_dDelta_part = take((size_t)P.n_slices * P.B * P.Hkv * P.d * P.H * sizeof(float));
   if (off > kNoAllocScratchBytes) return DMA_ERR_UNSUPPORTED;   // the problem needs more scratch
   void* scratch = nullptr;
-  if (scratch_address(&scratch) != cudaSuccess) return DMA_ERR_CUDA;
-  return launch_gate_bwd(Q, V, Delta, A, x_save, delta, d_delta, dDelta, dA, dV_gate, scratch,
-                         (cudaStream_t)stream) == cudaSuccess
-             ? DMA_OK
-             : DMA_ERR_CUDA;
+  const cudaError_t e = scratch_address(&scratch);
+  if (e != cudaSuccess) return cuda_status(e);
+  return cuda_status(launch_gate_bwd(Q, V, Delta, A, x_save, delta, d_delta, dDelta, dA, dV_gate, scratch,
+                                     (cudaStream_t)stream));
 }

@@ -131,7 +131,7 @@ dma_status_t dma_paged_append(const dma_params_t* p, const dma_pages_t* c, const
   a.T = T;
   a.starts = starts;
   a.q = q; a.k = k; a.v = v; a.Delta = Delta; a.A = A; a.Q = Q;
-  return launch_paged_append(P, a, workspace, (cudaStream_t)stream) == cudaSuccess ? DMA_OK : DMA_ERR_CUDA;
+  return cuda_status(launch_paged_append(P, a, workspace, (cudaStream_t)stream));
 }
 
 dma_status_t dma_paged_topk(const dma_params_t* p, const dma_pages_t* c, void* workspace, size_t workspace_bytes,
@@ -140,7 +140,7 @@ dma_status_t dma_paged_topk(const dma_params_t* p, const dma_pages_t* c, void* w
   dma_status_t st = paged_plan(p, c, &P);
   if (st != DMA_OK) return st;
   if ((st = check_ws(P, workspace, workspace_bytes)) != DMA_OK) return st;
-  return launch_paged_topk(P, workspace, (cudaStream_t)stream) == cudaSuccess ? DMA_OK : DMA_ERR_CUDA;
+  return cuda_status(launch_paged_topk(P, workspace, (cudaStream_t)stream));
 }
 
 dma_status_t dma_paged_attn(const dma_params_t* p, const dma_pages_t* c, const void* Q, void* workspace,
@@ -150,7 +150,7 @@ dma_status_t dma_paged_attn(const dma_params_t* p, const dma_pages_t* c, const v
   if (st != DMA_OK) return st;
   if (!ok_ptr(Q) || !ok_ptr(O) || !ok_ptr(LSE)) return DMA_ERR_INVALID_ARG;
   if ((st = check_ws(P, workspace, workspace_bytes)) != DMA_OK) return st;
-  return launch_paged_attn(P, Q, workspace, O, LSE, (cudaStream_t)stream) == cudaSuccess ? DMA_OK : DMA_ERR_CUDA;
+  return cuda_status(launch_paged_attn(P, Q, workspace, O, LSE, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -338,7 +338,7 @@ dma_status_t dma_prep(const dma_params_t* p, const dma_prep_t* r, const dma_prep
     a.stride[1][i] = st->k[i];
     a.stride[2][i] = v != nullptr ? st->v[i] : 0;
   }
-  return launch_prep_fwd(a, bf16, p->d, (cudaStream_t)stream) == cudaSuccess ? DMA_OK : DMA_ERR_CUDA;
+  return cuda_status(launch_prep_fwd(a, bf16, p->d, (cudaStream_t)stream));
 }
 
 dma_status_t dma_prep_workspace_size(const dma_params_t* p, const dma_prep_t* r, size_t* bytes) {
@@ -387,8 +387,7 @@ dma_status_t dma_prep_bwd(const dma_params_t* p, const dma_prep_t* r, const dma_
     a.gstride[1][i] = gst->k[i];
     a.gstride[2][i] = dv != nullptr ? gst->v[i] : 0;
   }
-  return launch_prep_bwd(a, bf16, p->d, dq_weight, dk_weight, (cudaStream_t)stream) == cudaSuccess ? DMA_OK
-                                                                                                   : DMA_ERR_CUDA;
+  return cuda_status(launch_prep_bwd(a, bf16, p->d, dq_weight, dk_weight, (cudaStream_t)stream));
 }
 
 }  // extern "C"
