@@ -91,3 +91,17 @@ def test_pages_of_another_device_are_refused(lib, monkeypatch):
     with pytest.raises(ValueError, match="cuda:1"):
         dma.paged_topk(_params(), c, torch.zeros(64, dtype=torch.uint8))
     assert lib.calls == []
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_parameters_are_looked_at_again_when_they_change(lib, name):
+    p = _params()
+    c = _pages(p)
+    _calls(p, c)[name]()
+    p.B = 4
+    with pytest.raises(ValueError, match="pages"):
+        _calls(p, c)[name]()
+    assert lib.calls == [name]
+    p.B = 2
+    _calls(p, c)[name]()
+    assert lib.calls == [name, name]

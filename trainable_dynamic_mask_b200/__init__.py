@@ -71,9 +71,7 @@ def _ptr(t):
 
 
 def _nbytes(t):
-    if t is None:
-        return 0
-    return t.numel() * t.element_size()
+    return 0 if t is None else t.nbytes
 
 
 def _stream(stream):
@@ -330,13 +328,8 @@ def make_pages(p, K, V, delta, table, lens, prefix=0) -> DmaPages:
                  lens=_dense("lens", lens, (p.B,), tt.i32, dev), n_pages=n, page=page,
                  max_pages=table.shape[1], prefix=int(prefix))
     c.tensors, c.device = (K, V, delta, table, lens), dev
-    c.sequences, c.rows = p.B, (p.H, p.Hkv, p.d, p.dtype)
+    c.sequences, c.rows, c.fits = p.B, (p.H, p.Hkv, p.d, p.dtype), (None, None)
     return c
-
-
-def _same_device(c, dev):
-    if c.device != dev:
-        raise ValueError(f"the pages are on cuda:{c.device}, the current device is cuda:{dev}")
 
 
 def _same_problem(p, c):
@@ -345,6 +338,18 @@ def _same_problem(p, c):
     if p.B > c.sequences or (p.H, p.Hkv, p.d, p.dtype) != c.rows:
         raise ValueError(f"the pages were made for B <= {c.sequences} and (H, Hkv, d, dtype) = {c.rows}, not for "
                          f"B = {p.B} and {(p.H, p.Hkv, p.d, p.dtype)}")
+
+
+def _check_pages(p, c, dev):
+    """(B, H, Hkv, d, storage type) of p, whose pages fit it (looked at again when any field of p changes) and
+    are on the current device dev."""
+    if c.device != dev:
+        raise ValueError(f"the pages are on cuda:{c.device}, the current device is cuda:{dev}")
+    key, fits = bytes(p), c.fits
+    if fits[0] != key:
+        _same_problem(p, c)
+        c.fits = fits = key, (p.B, p.H, p.Hkv, p.d, _torch().types[p.dtype])
+    return fits[1]
 
 
 def paged_layout(p, c) -> DmaPagedLayout:
@@ -362,14 +367,12 @@ def paged_append(p, c, r, q, k, v, Delta, A, Q, workspace, starts=None, stream=N
     normed and rotated queries (q and Q may be None together).  starts: device int32 [B + 1], the
     sequences' token ranges; None: one token each."""
     call, tt = load().dma_paged_append, _torch()
-    dev, t, f = tt.device(), tt.types[p.dtype], tt.f32
-    T, H, Hkv, d = k.shape[0], p.H, p.Hkv, p.d
-    _same_device(c, dev)
-    _same_problem(p, c)
+    dev, f, T = tt.device(), tt.f32, k.shape[0]
+    B, H, Hkv, d, t = _check_pages(p, c, dev)
     _check_prep_tensors(p, r, dev)
     st = DmaPrepStrides()
     check("dma_paged_append", call(
-        p, c, r, st, T, _dense("starts", starts, (p.B + 1,), tt.i32, dev),
+        p, c, r, st, T, _dense("starts", starts, (B + 1,), tt.i32, dev),
         _rows("q", q, (T, H, d), t, dev, st.q), _rows("k", k, (T, Hkv, d), t, dev, st.k),
         _rows("v", v, (T, Hkv, d), t, dev, st.v), _dense("Delta", Delta, (Hkv * d, H), t, dev),
         _dense("A", A, (H,), f, dev), _dense("Q", Q, (T, H, d), t, dev), _workspace(workspace, dev),
@@ -380,22 +383,21 @@ def paged_topk(p, c, workspace, stream=None):
     """Selection of every (sequence, head) over its cache, into the workspace."""
     call, tt = load().dma_paged_topk, _torch()
     dev = tt.device()
-    _same_device(c, dev)
-    _same_problem(p, c)
+    _check_pages(p, c, dev)
     check("dma_paged_topk", call(p, c, _workspace(workspace, dev), _nbytes(workspace),
-                                                  tt.stream(dev) if stream is None else _stream(stream)))
+                                 tt.stream(dev) if stream is None else _stream(stream)))
 
 
 def paged_attn(p, c, Q, workspace, O, LSE, stream=None):
     """Attention of one query [B, H, d] for each sequence over the keys paged_topk selected."""
     call, tt = load().dma_paged_attn, _torch()
-    dev, t = tt.device(), tt.types[p.dtype]
-    shape = (p.B, p.H, p.d)
-    _same_device(c, dev)
-    _same_problem(p, c)
+    dev = tt.device()
+    B, H, _, d, t = _check_pages(p, c, dev)
+    shape = (B, H, d)
     check("dma_paged_attn", call(
         p, c, _dense("Q", Q, shape, t, dev), _workspace(workspace, dev), _nbytes(workspace),
-        _dense("O", O, shape, t, dev), _dense("LSE", LSE, (p.B, p.H), tt.f32, dev), tt.stream(dev) if stream is None else _stream(stream)))
+        _dense("O", O, shape, t, dev), _dense("LSE", LSE, (B, H), tt.f32, dev),
+        tt.stream(dev) if stream is None else _stream(stream)))
 
 
 # ---------------------------------------------------------------- convenience (torch allocation)
