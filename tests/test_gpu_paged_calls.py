@@ -48,3 +48,114 @@ def test_append_fills_the_prefix_through_one_sequence():
     _call(c, a)
     assert c.dma.check_device_status(c.p, c.ws) == 0
     _check_append(c, a, 64, False, before)
+
+
+SHAPES = {
+    "rows": ([700, 0, 33, 512, 90], 0, 4, 2, 64, 16, "bf16", 64),
+    "few_behind_prefix": ([320, 333, 0, 500, 320], 320, 4, 2, 128, 64, "bf16", 100),
+    "many_behind_prefix": ([1280 + 7 * (i % 9) for i in range(40)], 1280, 16, 4, 64, 64, "bf16", 1200),
+    "long_rows": ([20000 - 117 * i for i in range(12)], 0, 16, 1, 64, 64, "bf16", 150),
+}
+
+
+def _make(name, seed=71):
+    lens, prefix, H, Hkv, d, page, dtype, w = SHAPES[name]
+    return Cache(lens, H, Hkv, d, page, dtype, w, seed=seed, prefix=prefix, N=max(lens) + 64)
+
+
+@pytest.mark.parametrize("name", SHAPES)
+def test_steps_in_flight_equal_steps_one_by_one(name):
+    """Lengths, gate values and queries change from call to call while earlier calls on the same workspace
+    still run."""
+    c = _make(name)
+    torch, dma = c.torch, c.dma
+    S, lens0 = len(c.lens_host), c.lens.clone()
+    deltas = [c.delta.clone(), c.delta.flip(0).contiguous(), (c.delta * 0.5).contiguous()]
+    Q = [c.normal(S, c.H, c.d).to(c.t) for _ in range(2)]
+    grow = [(lens0 + g) * (lens0 > 0) for g in (0, 40, 17, 63)]
+    results = []
+    for wait in (True, False):
+        out = [(torch.empty_like(Q[0]), torch.empty((S, c.H), device="cuda")) for _ in range(24)]
+        torch.cuda.synchronize()
+        for i, (O, L) in enumerate(out):
+            c.delta.copy_(deltas[i % 3])
+            c.lens.copy_(grow[i % 4])
+            dma.paged_topk(c.p, c.c, c.ws)
+            dma.paged_attn(c.p, c.c, Q[i % 2], c.ws, O, L)
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        results.append(out)
+    for a, b in zip(*results):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert dma.check_device_status(c.p, c.ws) == 0
+
+
+@pytest.mark.parametrize("name", SHAPES)
+def test_calls_captured_behind_another_streams_work(name):
+    """In a captured graph the calls follow copies and kernels of another stream, and run on a forked one."""
+    c = _make(name)
+    torch, dma = c.torch, c.dma
+    S = len(c.lens_host)
+    src = dict(delta=c.delta.flip(0).contiguous(), lens=(c.lens + 9) * (c.lens > 0),
+               Q=c.normal(S, c.H, c.d).to(c.t))
+    old = dict(delta=c.delta.clone(), lens=c.lens.clone())
+    Q = torch.zeros_like(src["Q"])
+    c.delta.copy_(src["delta"])
+    c.lens.copy_(src["lens"])
+    want = c.run(src["Q"])[1:]
+    want = [x.clone() for x in want]
+    O, L = torch.empty_like(want[0]), torch.empty_like(want[1])
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            c.delta.copy_(src["delta"])       # a copy
+            Q.copy_(src["Q"])
+        torch.mul(src["lens"], 1, out=c.lens)  # a kernel
+        main.wait_stream(side)                # the selection follows both
+        dma.paged_topk(c.p, c.c, c.ws)
+        O.zero_()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):         # the attention on the forked stream
+            dma.paged_attn(c.p, c.c, Q, c.ws, O, L)
+        main.wait_stream(side)
+    for _ in range(3):
+        c.delta.copy_(old["delta"])
+        c.lens.copy_(old["lens"])
+        Q.zero_()
+        L.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(O, want[0]) and torch.equal(L, want[1])
+    assert dma.check_device_status(c.p, c.ws) == 0
+
+
+def test_calls_from_two_host_threads():
+    import threading
+    a, b = _make("few_behind_prefix"), _make("rows", seed=72)
+    torch = a.torch
+    want = [a.run(), b.run()]
+    torch.cuda.synchronize()
+    got, errors = [None, None], []
+
+    def work(i, c):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(50):
+                    got[i] = c.run(want[i][0])
+            s.synchronize()
+        except Exception as e:
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(i, c)) for i, c in enumerate((a, b))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for w, g in zip(want, got):
+        for x, y in zip(w, g):
+            assert torch.equal(x, y)

@@ -158,7 +158,7 @@ constexpr int decode_smem_bytes() {
 // LSE = (M + log2 L) ln 2.  The splits' (m, l) are loaded one per thread into shared memory and
 // each channel's partials 16 at a time, so that the loads are in flight together.
 template <int D, typename OutT>
-__global__ void decode_combine_kernel(const float* __restrict__ part, OutT* __restrict__ O,
+__global__ void decode_combine_kernel(const float* part, OutT* __restrict__ O,
                                       float* __restrict__ LSE, int n_split) {
   extern __shared__ float cmb[];   // [n_split] m, then [n_split] l and later the weights
   float* sm_m = cmb;

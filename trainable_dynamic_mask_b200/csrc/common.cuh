@@ -113,6 +113,9 @@ inline cudaError_t ensure_smem_limit(Kernel k, int bytes) {
 // in the stream still runs, once that one's blocks have all called pdl_trigger (or ended); it calls pdl_wait,
 // in every thread that reads or writes global memory, before it does so: from there on all that came before
 // is complete.  What precedes pdl_wait (and the launch itself) then costs no time of its own.
+// What such a kernel reads may still be being written when it starts: its pointers to it are neither
+// __restrict__ nor read with __ldg, both of which let loads take the path for data that nobody writes while the
+// kernel runs.
 DMA_DEVINL void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 DMA_DEVINL void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

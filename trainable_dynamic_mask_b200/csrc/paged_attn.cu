@@ -78,9 +78,8 @@ template <typename T, int NT> constexpr int list_smem() { return kPlStages * lis
 // an SM.
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(NT, 512 / NT)
-paged_list_kernel(const T* __restrict__ Q, const T* __restrict__ K, const T* __restrict__ V,
-                  const int4* __restrict__ rows, const int2* __restrict__ ent, float* __restrict__ part,
-                  int32_t* __restrict__ counters, T* __restrict__ O, float* __restrict__ LSE, int H, int Hkv,
+paged_list_kernel(const T* Q, const T* K, const T* V, const int4* rows, const int2* ent, float* part,
+                  int32_t* counters, T* __restrict__ O, float* __restrict__ LSE, int H, int Hkv,
                   int page_shift, int n_slots, int sel_len, int n_split, int n_psplit, float scale) {
   constexpr int L = D / 8, RPW = 32 / L, NG = (NT / 32) * RPW;   // lanes of a row; groups of a warp, of the CTA
   constexpr int U = list_keys<T>(), NP = sizeof(T) / 2;         // 16-byte pieces of a lane's eight channels
@@ -285,10 +284,9 @@ template <int R> constexpr int cand_threads() { return R == 1 ? 128 : 256; }
 
 template <int D, int R>
 __global__ void __launch_bounds__(cand_threads<R>(), 2)
-paged_cand_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ K, const uint16_t* __restrict__ V,
-                  const int4* __restrict__ rows, const int32_t* __restrict__ crow, const int2* __restrict__ cent,
-                  float* __restrict__ part, int B, int H, int Hkv, int page_shift, int n_slots, int cand_len, int cand_split,
-                  int n_part, float scale) {
+paged_cand_kernel(const uint16_t* Q, const uint16_t* K, const uint16_t* V, const int4* rows, const int32_t* crow,
+                  const int2* cent, float* __restrict__ part, int B, int H, int Hkv, int page_shift, int n_slots,
+                  int cand_len, int cand_split, int n_part, float scale) {
   constexpr int kPcThreads = cand_threads<R>(), kPcWarps = kPcThreads / 32;
   constexpr int CH = D / 8, KG = kPcWarps / R, NT = 8 / KG, NO = D / 8;   // NT, NO: 8-wide tiles of keys, channels
   extern __shared__ __align__(128) unsigned char csm[];
@@ -553,8 +551,9 @@ cudaError_t launch_list_t(const PagedPlan& P, const void* Q, void* ws, void* O, 
   const cudaError_t e = ensure_smem_limit(paged_list_kernel<T, D, NT>, list_smem<T, NT>());
   if (e != cudaSuccess) return e;
   return launch_after(
-      paged_list_kernel<T, D, NT>, dim3(P.n_split, P.B * P.H), NT, list_smem<T, NT>(), s, 1, (const T*)Q, (const T*)P.K, (const T*)P.V, ws_ptr<int4>(ws, P.off_rows), ws_ptr<int2>(ws, P.off_ent),
-      ws_ptr<float>(ws, P.off_part), ws_ptr<int32_t>(ws, P.off_count), (T*)O, LSE, P.H, P.Hkv, P.page_shift, P.n_pages << P.page_shift, P.sel_len,
+      paged_list_kernel<T, D, NT>, dim3(P.n_split, P.B * P.H), NT, list_smem<T, NT>(), s, 1, (const T*)Q, (const T*)P.K,
+      (const T*)P.V, ws_ptr<int4>(ws, P.off_rows), ws_ptr<int2>(ws, P.off_ent), ws_ptr<float>(ws, P.off_part),
+      ws_ptr<int32_t>(ws, P.off_count), (T*)O, LSE, P.H, P.Hkv, P.page_shift, P.n_pages << P.page_shift, P.sel_len,
       P.n_split, P.n_psplit, P.scale);
 }
 

@@ -69,10 +69,9 @@ DMA_DEVINL void pv_steps(uint32_t d, uint32_t a, uint64_t dv, uint32_t id, uint3
 
 template <int D>
 __global__ void __launch_bounds__(kCtThreads, 1)
-paged_cand_tc_kernel(const uint16_t* __restrict__ Q, const uint16_t* __restrict__ K, const uint16_t* __restrict__ V,
-                     const int4* __restrict__ rows, const int32_t* __restrict__ crow, const int2* __restrict__ cent,
-                     float* __restrict__ part, int32_t* __restrict__ status, int B, int H, int Hkv, int page_shift,
-                     int n_slots, int cand_len, int cand_split, int n_part, float scale) {
+paged_cand_tc_kernel(const uint16_t* Q, const uint16_t* K, const uint16_t* V, const int4* rows, const int32_t* crow,
+                     const int2* cent, float* __restrict__ part, int32_t* __restrict__ status, int B, int H, int Hkv,
+                     int page_shift, int n_slots, int cand_len, int cand_split, int n_part, float scale) {
   using S = CtSmem<D>;
   constexpr int CH = D / 8;
   extern __shared__ __align__(1024) unsigned char raw[];

@@ -95,7 +95,7 @@ DMA_DEVINL bool rest_by_tail(const PagedPlan& P, const int32_t* tab, int h, int 
     uint32_t k[4] = {0u, 0u, 0u, 0u};
     bool wrong = false;
     if (pos < len) {
-      const int pg = __ldg(tab + (pos >> P.page_shift));
+      const int pg = tab[pos >> P.page_shift];
       wrong = pg < 0 || pg >= P.n_pages;
       if (!wrong) {
         const float4 f = *reinterpret_cast<const float4*>(head + ((size_t)(unsigned)(pg * P.H) << P.page_shift) +
@@ -152,7 +152,7 @@ DMA_DEVINL bool rest_by_tail(const PagedPlan& P, const int32_t* tab, int h, int 
   __syncthreads();
   if (tid < m && in) {
     const int at = (tid >= 32 ? buf[0] : 0) + __popc(mine & ((1u << lane) - 1u));
-    const int pos = where[tid], pg = __ldg(tab + (pos >> P.page_shift));
+    const int pos = where[tid], pg = tab[pos >> P.page_shift];
     const uint32_t k = keys[tid];
     lp[at] = pos;
     le[at] = make_int2((pg << P.page_shift) + (pos & (page - 1)), (int)((k & 0x80000000u) ? k ^ 0x80000000u : ~k));
@@ -170,9 +170,8 @@ DMA_DEVINL bool rest_by_tail(const PagedPlan& P, const int32_t* tab, int h, int 
 template <SelMode M, int NT, bool SIEVE, int MC>
 __global__ void __launch_bounds__(NT, NT == 512 ? 2 : NT == 256 ? 4 : 8)
 paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict__ sel, int2* __restrict__ ent,
-                    int32_t* __restrict__ crow, int32_t* __restrict__ cand, int2* __restrict__ cent,
-                    int2* __restrict__ tail, int32_t* __restrict__ counters, int32_t* __restrict__ status, int cap, int page_cap,
-                    int list_cap, bool longest_first) {
+                    int32_t* crow, int32_t* __restrict__ cand, int2* cent, int2* tail, int32_t* __restrict__ counters,
+                    int32_t* __restrict__ status, int cap, int page_cap, int list_cap, bool longest_first) {
   constexpr int NW = NT / 32, BINS = 4 * NT, LB = NT == 512 ? 11 : NT == 256 ? 10 : 9;
   static_assert(BINS == 1 << LB, "four counters a thread");
   static_assert(!SIEVE || M == kRows, "candidates and their rest are short or few");
@@ -210,11 +209,11 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
     if (tid == 0) place = want;
     __syncthreads();
     for (int t = tid; t < P.B; t += NT) {
-      const int n = __ldg(P.lens + t);
+      const int n = P.lens[t];
       int before = 0;
 #pragma unroll 8
       for (int u = 0; u < P.B; ++u) {
-        const int o = __ldg(P.lens + u);
+        const int o = P.lens[u];
         before += o > n || (o == n && u < t);
       }
       if (before == want) place = t;
@@ -229,7 +228,7 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
 
   // ---- the row: indices [0, n1) candidates, [n1, n1p) nothing, [n1p, n) positions base + (i - n1p)
   const int base = M == kRest ? P.prefix : 0;
-  int n1 = 0, len = M == kCandidates ? P.prefix : __ldg(P.lens + b);
+  int n1 = 0, len = M == kCandidates ? P.prefix : P.lens[b];
   bool bad = false;
   if (M == kRest) {
     n1 = crow[h];
@@ -258,7 +257,7 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
   const int tab0 = (base + max(i0 - n1p, 0)) >> P.page_shift;
   const int np = i1 > n1p && i1 > i0 ? ((base + i1 - 1 - n1p) >> P.page_shift) - tab0 + 1 : 0;
   for (int i = tid; i < min(np, page_cap); i += NT) {
-    int pg = __ldg(tab + tab0 + i);
+    int pg = tab[tab0 + i];
     if (pg < 0 || pg >= P.n_pages) {
       bad = true;
       pg = 0;
@@ -282,7 +281,7 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
   auto page_of = [&](int pos) -> int {
     const int i = (pos >> P.page_shift) - tab0;
     if (i < page_cap) return pages[i];
-    int pg = __ldg(tab + tab0 + i);
+    int pg = tab[tab0 + i];
     if (pg < 0 || pg >= P.n_pages) {
       bad = true;
       pg = 0;
@@ -923,8 +922,11 @@ cudaError_t launch_select_t(const PagedPlan& P, int n_rows, int n, int C, int ca
   const size_t smem = (size_t)(cap + page_cap) * 4;
   const cudaError_t e = ensure_smem_limit(paged_select_kernel<M, NT, SIEVE, MC>, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_after(paged_select_kernel<M, NT, SIEVE, MC>, dim3(C, n_rows), NT, smem, s, MC > 1 ? C : 1,
-                      P, ws_ptr<int32_t>(ws, P.off_rows), ws_ptr<int32_t>(ws, P.off_sel), ws_ptr<int2>(ws, P.off_ent), ws_ptr<int32_t>(ws, P.off_crow), ws_ptr<int32_t>(ws, P.off_cand), ws_ptr<int2>(ws, P.off_cent), ws_ptr<int2>(ws, P.off_tail), ws_ptr<int32_t>(ws, P.off_count), ws_ptr<int32_t>(ws, P.off_status), cap, page_cap, list_cap,
+  return launch_after(paged_select_kernel<M, NT, SIEVE, MC>, dim3(C, n_rows), NT, smem, s, MC > 1 ? C : 1, P,
+                      ws_ptr<int32_t>(ws, P.off_rows), ws_ptr<int32_t>(ws, P.off_sel), ws_ptr<int2>(ws, P.off_ent),
+                      ws_ptr<int32_t>(ws, P.off_crow), ws_ptr<int32_t>(ws, P.off_cand), ws_ptr<int2>(ws, P.off_cent),
+                      ws_ptr<int2>(ws, P.off_tail), ws_ptr<int32_t>(ws, P.off_count),
+                      ws_ptr<int32_t>(ws, P.off_status), cap, page_cap, list_cap,
                       M == kRows && P.B > 1 && P.B <= 256 && n_rows * NT > sm_count() * 1024);
 }
 

@@ -183,8 +183,8 @@ prep_bwd_kernel(const __grid_constant__ PrepArgs a, int wt) {
 // dg[c] = sum over blocks, in double precision: at most kPrepMaxBlocks terms per channel.  A block takes
 // eight channels (a 32-byte sector of every partial row), so that a thread has only a few loads to wait for.
 __global__ void __launch_bounds__(1024)
-prep_reduce_kernel(const float* __restrict__ part, float* __restrict__ dq_weight, float* __restrict__ dk_weight,
-                   int n_blocks, int D) {
+prep_reduce_kernel(const float* part, float* __restrict__ dq_weight, float* __restrict__ dk_weight, int n_blocks,
+                   int D) {
   __shared__ double red[32][8];
   const int tid = threadIdx.x, c = blockIdx.x * 8 + (tid & 7), w = tid >> 3;
   float* out = blockIdx.y == 0 ? dq_weight : dk_weight;
