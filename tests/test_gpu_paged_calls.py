@@ -159,3 +159,16 @@ def test_calls_from_two_host_threads():
     for w, g in zip(want, got):
         for x, y in zip(w, g):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("B", [79, 80, 81, 130])
+def test_rows_of_several_rounds(B):
+    """More rows than the GPU takes at once, with and without an order by lengths: long, equal, idle and bad ones."""
+    lens = [(i * 977) % 4300 for i in range(B - 7)] + [0, 0, 4300, 4300, 1, 1, 2]
+    c = Cache(lens, 12, 4, 64, 16, "bf16", 40, seed=B)
+    c.lens[3] = 4301
+    c.dma.paged_topk(c.p, c.c, c.ws)
+    c.torch.cuda.synchronize()
+    assert c.dma.check_device_status(c.p, c.ws) == 0x10000000
+    c.lens_host[3] = 0
+    c.check_selection()
