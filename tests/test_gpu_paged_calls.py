@@ -172,3 +172,31 @@ def test_rows_of_several_rounds(B):
     assert c.dma.check_device_status(c.p, c.ws) == 0x10000000
     c.lens_host[3] = 0
     c.check_selection()
+
+
+@pytest.mark.parametrize("d,Hkv,prefix,w,most", [(64, 2, 8192, 1024, 304), (128, 8, 4096, 512, 400), (128, 1, 4096, 512, 600)])
+def test_many_rows_behind_a_prefix(d, Hkv, prefix, w, most):
+    """Rows enough for lists of one warp each (and, where they are longer, not): none, few, and more own keys than one
+    partial result holds."""
+    B, H = 80, 16
+    lens = [0 if b % 13 == 5 else prefix + (b * 37) % most for b in range(B - 2)] + [prefix + most, prefix]
+    c = Cache(lens, H, Hkv, d, 16, "bf16", w, seed=d + Hkv, prefix=prefix, N=prefix + most,
+              w_heads=[w, 1, 0, 17, 64, 255, 256, 300, w - 1] + [w] * 7)
+    for b in (1, 7, B - 2):   # all their own keys pass
+        c.delta[c.table[b, prefix // 16:].long()] += 1.0
+    out = c.run()
+    c.torch.cuda.synchronize()
+    rows = c.region(c.dma.paged_layout(c.p, c.c).off_rows, (B, H, 4))
+    assert rows[B - 2, 0, 0] == min(w, most) and rows[B - 1, 0, 0] == 0
+    got = c.selected()
+    again = c.run(out[0])
+    for x, y in zip(out, again):
+        assert c.torch.equal(x, y)
+    # the definition, for some of the sequences
+    some = sorted({*range(0, B, 9), 1, 5, 7, B - 2, B - 1})
+    c.lens_host, c.table = [lens[b] for b in some], c.table[some]
+    for i, b in enumerate(some):
+        _, _, delta = c.row(i)
+        for h in range(H):
+            np.testing.assert_array_equal(got[b][h], c.chosen(delta[h], h), err_msg=f"{b} {h}")
+    c.check(out[0][some], out[1][some], out[2][some])

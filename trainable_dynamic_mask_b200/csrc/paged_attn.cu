@@ -559,9 +559,11 @@ cudaError_t launch_list_t(const PagedPlan& P, const void* Q, void* ws, void* O, 
 
 template <typename T, int D>
 cudaError_t launch_list(const PagedPlan& P, const void* Q, void* ws, void* O, float* LSE, cudaStream_t s) {
-  // behind a shared prefix a row lists about w (N - prefix) / N keys; one warp is enough for few of them, if
-  // there are rows enough to fill the GPU with such CTAs: 2048 rows of some 15 keys 9.5 us, with 128 threads 17.7
-  if (P.shared && P.B * P.H >= 8 * sm_count() && (int64_t)P.w * (P.N - P.prefix) <= (int64_t)64 * P.N)
+  // Behind a shared prefix a row lists about w (N - prefix) / N keys; one warp is enough for few of them, if there are
+  // rows enough to fill the GPU with such CTAs.  The attention of 2048 rows, with one warp and with 128 threads, at
+  // some 8 keys a row 21.7 us and 28.3, 14 33.6 and 38.6, 42 38.8 and 41.4, 48 34.6 and 34.0, 56 36.8 and 34.6, 64 47.1
+  // and 44.7; of rows of 16 keys, 512 17.8 and 14.1, 1024 20.9 and 20.8, 1280 21.7 and 24.0.
+  if (P.shared && P.B * P.H >= 8 * sm_count() && (int64_t)P.w * (P.N - P.prefix) <= (int64_t)48 * P.N)
     return launch_list_t<T, D, 32>(P, Q, ws, O, LSE, s);
   return launch_list_t<T, D, 128>(P, Q, ws, O, LSE, s);
 }
