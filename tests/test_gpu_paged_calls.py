@@ -200,3 +200,31 @@ def test_many_rows_behind_a_prefix(d, Hkv, prefix, w, most):
         for h in range(H):
             np.testing.assert_array_equal(got[b][h], c.chosen(delta[h], h), err_msg=f"{b} {h}")
     c.check(out[0][some], out[1][some], out[2][some])
+
+
+@pytest.mark.parametrize("H,Hkv,d,dtype", [(16, 4, 64, "bf16"), (32, 2, 64, "bf16"), (48, 2, 64, "bf16"), (64, 8, 128, "bf16"),
+                                           (33, 3, 64, "f32")])
+def test_a_prompt_in_parts_is_the_prompt_at_once(H, Hkv, d, dtype):
+    """Tokens enough for several rounds of CTAs, against the same tokens in calls of a few: the same bits."""
+    lens = [3500, 0, 1621]
+    c = Cache(lens, H, Hkv, d, 64, dtype, 8, seed=H, N=3600)
+    torch = c.torch
+    a = _append(c, lens, d, False, True, pad=5)
+    before = [x.clone() for x in (c.K, c.V, c.delta)]
+    _call(c, a)
+    whole = [x.clone() for x in (c.K, c.V, c.delta, a["Q"])]
+    for x, y in zip((c.K, c.V, c.delta), before):
+        x.copy_(y)
+    Q, at, first = torch.full_like(a["Q"], 9.0), [0, 0, 0], [0, 3500, 3500]
+    for n in (1, 700, 37, 2000, 64, 3500):
+        take = [min(n, lens[b] - at[b]) for b in range(3)]
+        tok = torch.cat([torch.arange(first[b] + at[b], first[b] + at[b] + take[b], device="cuda") for b in range(3)])
+        at = [x + t for x, t in zip(at, take)]
+        c.lens.copy_(torch.tensor(at, dtype=torch.int32))
+        part = dict(a, starts=torch.tensor(np.concatenate([[0], np.cumsum(take)]), dtype=torch.int32, device="cuda"),
+                    Q=torch.empty((tok.numel(), H, d), dtype=c.t, device="cuda"), **{k: a[k][tok] for k in "qkv"})
+        _call(c, part)
+        Q[tok] = part["Q"]
+    assert at == lens and c.dma.check_device_status(c.p, c.ws) == 0
+    for x, y in zip(whole, (c.K, c.V, c.delta, Q)):
+        assert torch.equal(x, y)

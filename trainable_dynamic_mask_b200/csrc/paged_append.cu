@@ -4,16 +4,18 @@
 //
 // One kernel, two kinds of CTAs side by side: the first walk over the rows (rows.cuh, as in prep.cu), the
 // others form the gate's product (the values of 16 tokens against Delta, tensor cores for bf16).  The walk's
-// shares are fixed when it starts and it is the longer way, so it comes first, with three CTAs an SM and two
-// chunks of rows on their way; the gate's CTAs follow where those have ended.
+// shares are fixed when it starts and it is the longer way, so it comes first, with three CTAs an SM (two for more
+// than 32 heads in bf16) and two chunks of rows on their way; the gate's CTAs follow where those have ended.
 //
 // Bytes: each projection read once and each row written once, 16 KB a token at 16 + 8 + 8 heads of 128
-// channels in bf16, Delta from L2.  5037 tokens of 5 prompts take 25.7 us (3.2 TB/s); without the gate they
-// would take 4 us less, the gate alone 9.  What is left is a short call's: a plain copy of as many bytes
-// stays a third below its rate for long ones.  Two CTAs an SM with four chunks on their way took 28.6 us,
-// three with four 27.5, four (64 registers) 29; the gate's CTAs first, or with four stages, the same.
-// One token for each of 8 sequences takes 8.5 us in a graph, bound by latency: the lookup's reads, one wave of
-// rows, the gate (3 us of it).
+// channels in bf16, Delta from L2.  5037 tokens of 5 prompts take 25.6 us among calls on other inputs (3.2 TB/s) and
+// 34 in a graph from a cold L2, where a plain copy of as many bytes takes 37: a short call stays below a long
+// one's rate.  Without the gate they would take 4 us less, the gate alone 9.  Two CTAs an SM with four chunks on
+// their way took 28.6 us, three with four 27.5, four (64 registers) 29; the gate's CTAs first, or with four stages,
+// the same.  float32, 32 + 8 + 8 heads: 126 us (floor 38); the gate's product on the FMA pipe reads Delta from L2
+// for every 8 tokens.
+// One token for each of 64 sequences takes 9 us in a graph, bound by latency: the lookup's reads, one wave of
+// rows, the gate (3 us of it); in float32 34.
 #include "rows.cuh"
 
 namespace dma {
@@ -315,9 +317,11 @@ paged_append_kernel(const __grid_constant__ PrepArgs w, const __grid_constant__ 
 
 template <typename T, int D, int HT>
 cudaError_t launch_append(const PrepArgs& w, const SlotDest& d, cudaStream_t s) {
+  // the gate's stages for more than 32 heads leave room for two CTAs an SM, so the rows' shares are made for two (5037
+  // tokens of 64 heads: 80.8 us, in shares for three 88.3)
   int wt;
-  const int row_blocks = walk_blocks(d.a.T, 3, &wt), tok = HT > 0 ? kAgTok : kAfTok;
-  constexpr int smem = append_smem<T, HT>();
+  constexpr int smem = append_smem<T, HT>(), per_sm = smem > 64 * 1024 ? 2 : 3;
+  const int row_blocks = walk_blocks(d.a.T, per_sm, &wt), tok = HT > 0 ? kAgTok : kAfTok;
   auto kernel = w.inter ? paged_append_kernel<T, D, true, HT> : paged_append_kernel<T, D, false, HT>;
   const cudaError_t e = ensure_smem_limit(kernel, smem);
   if (e != cudaSuccess) return e;
