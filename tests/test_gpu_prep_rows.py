@@ -2,7 +2,8 @@
 
 With a single row of dQ (dK) that is not zero the sum over all rows is that row's own term, however the rows are
 shared out: every other addition adds a zero.  The term dy x r is off by what its factors are (see
-test_gpu_prep.py): 40 u of its magnitude covers them, and the final rounding to float32 one u more."""
+test_gpu_prep.py): 40 u of (|a| + |b|) |x| r, a and b the pair that was rotated into dy, covers them, and the final
+rounding to float32 one u more."""
 import numpy as np
 import pytest
 
@@ -39,7 +40,10 @@ def test_every_row_counts_once(B, N, H, Hkv, d, dtype, rot, inter):
         one = dict(c, pos=torch.tensor([[n]], dtype=torch.int32))
         R = _R(one, 1, 1, d)
         for got, x, w, dy, h in ((dqw, c["q"], c["qw"], row[0], hq), (dkw, c["k"], c["kw"], row[1], hk)):
-            _, _, ref, mag = _backward(_np(x[b, n, h])[None, None, None], _np(w), R, eps, _np(dy)[None, None, None])
+            x, dy = _np(x[b, n, h]), _np(dy)
+            _, _, ref, _ = _backward(x[None, None, None], _np(w), R, eps, dy[None, None, None])
+            pairs = np.abs(dy) @ (R[0, 0] != 0)
+            mag = pairs * np.abs(x) / np.sqrt((x * x).mean() + eps)
             err = np.abs(_np(got) - ref)
             assert (err <= 41 * U * mag).all(), (n, h, (err / mag).max() / U)
         # the row's own gradient is the only one
