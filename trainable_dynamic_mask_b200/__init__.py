@@ -13,8 +13,8 @@ from __future__ import annotations
 
 import ctypes
 
-from ._lib import (BLOCK_Q, DMA_BF16, DMA_F32, DMA_FLAG_FORWARD_ONLY, DmaCpLayout, DmaError, DmaPagedLayout, DmaPages, DmaParams,
-                   DmaPrep, DmaPrepStrides, DmaWsLayout, LIB_PATH, check, exported_names, load)
+from ._lib import (BLOCK_Q, DMA_BF16, DMA_F32, DMA_FLAG_FORWARD_ONLY, DmaCpLayout, DmaError, DmaPagedLayout, DmaPages,
+                   DmaParams, DmaPrep, DmaPrepStrides, DmaWsLayout, LIB_PATH, check, exported_names, load)
 
 __all__ = [
     "BLOCK_Q", "DMA_BF16", "DMA_F32", "DmaError", "DmaParams", "LIB_PATH", "load", "exported_names",
@@ -272,7 +272,8 @@ def prep(p, r, q, k, v, Q, K, V, stream=None):
     check("dma_prep", call(
         p, r, st, _rows("q", q, (B, N, H, d), t, dev, st.q), _rows("k", k, (B, N, Hkv, d), t, dev, st.k),
         _rows("v", v, (B, N, Hkv, d), t, dev, st.v), _dense("Q", Q, (B, H, N, d), t, dev),
-        _dense("K", K, (B, Hkv, N, d), t, dev), _dense("V", V, (B, Hkv, N, d), t, dev), tt.stream(dev) if stream is None else _stream(stream)))
+        _dense("K", K, (B, Hkv, N, d), t, dev), _dense("V", V, (B, Hkv, N, d), t, dev),
+        tt.stream(dev) if stream is None else _stream(stream)))
 
 
 def prep_workspace_size(p, r) -> int:

@@ -105,7 +105,7 @@ bool make_tile_map(void* map, const void* base, uint64_t rows, int d, int box_ro
 int sm_count();   // SMs of the current device
 
 // ---------------------------------------------------------------- projections to inputs (prep.cu)
-constexpr int kPrepMaxBlocks = 592;   // 4 blocks an SM: rows of partial sums of the backward's workspace
+constexpr int kPrepMaxBlocks = 592;   // rows of partial sums in the backward's workspace; it launches two blocks an SM
 // Arguments of the kernels of dma_prep and dma_prep_bwd; [3] = query, key, value.
 struct PrepArgs {
   const float* inv_freq;
@@ -132,6 +132,7 @@ cudaError_t launch_prep_bwd(const PrepArgs& a, bool bf16, int d, float* dq_weigh
 constexpr int kPagedErr = 0x10000000;   // status bit: a page number or a length out of range
 constexpr int kPagedSplit = 256;        // selected keys per CTA of the attention over one row's list
 constexpr int kPagedTail = 64;          // last candidates of a shared prefix that are kept in order
+constexpr int kPagedMostKept = 4096;    // min(w, N) / d at most: decode's limit, as stated in dma.h
 
 // Resolved paged problem: what the kernels read, and the workspace plan.
 struct PagedPlan {

@@ -16,9 +16,10 @@ dma_status_t paged_plan(const dma_params_t* p, const dma_pages_t* c, PagedPlan* 
   if (!ok_ptr(c->K) || !ok_ptr(c->V) || !ok_ptr(c->delta) || !ok_ptr(c->table) || !ok_ptr(c->lens))
     return DMA_ERR_INVALID_ARG;
   if (c->n_pages < 1 || c->max_pages < 1 || c->page < 1 || c->prefix < 0) return DMA_ERR_INVALID_ARG;
-  if ((p->w < p->N ? p->w : p->N) > 4096 * p->d) return DMA_ERR_UNSUPPORTED;
+  if ((p->w < p->N ? p->w : p->N) > kPagedMostKept * p->d) return DMA_ERR_UNSUPPORTED;
   if (c->page < 16 || c->page > 1024 || (c->page & (c->page - 1)) != 0) return DMA_ERR_UNSUPPORTED;
-  if ((int64_t)c->n_pages * c->page >= ((int64_t)1 << 31) || (int64_t)c->n_pages * p->H >= ((int64_t)1 << 31)) return DMA_ERR_UNSUPPORTED;
+  if ((int64_t)c->n_pages * c->page >= ((int64_t)1 << 31) || (int64_t)c->n_pages * p->H >= ((int64_t)1 << 31))
+    return DMA_ERR_UNSUPPORTED;
   if (p->N > (int64_t)c->max_pages * c->page || c->prefix % c->page != 0 || c->prefix > p->N)
     return DMA_ERR_INVALID_ARG;
   memset(P, 0, sizeof(*P));

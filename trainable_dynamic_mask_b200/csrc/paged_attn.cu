@@ -274,9 +274,9 @@ template <int... I, typename F> DMA_DEVINL void each_of(std::integer_sequence<in
 template <int N, typename F> DMA_DEVINL void each(F f) { each_of(std::make_integer_sequence<int, N>(), f); }
 
 // CTA = (part of a head's candidates, head, 16 R sequences), R = 1 or 2.  Its 4 R warps are R groups of 16
-// sequences times 4 groups of keys.  Tiles of 64 candidates' K and V rows are gathered with 16-byte asynchronous copies (swizzled by row, conflict-free for ldmatrix), one tile
-// ahead.  A weight is split into two bf16 parts, both multiplied with V: one part alone would round every
-// weight to 8 bits, as much as the output's own rounding.
+// sequences times 4 groups of keys.  Tiles of 64 candidates' K and V rows are gathered with 16-byte asynchronous
+// copies (swizzled by row, conflict-free for ldmatrix), one tile ahead.  A weight is split into two bf16 parts, both
+// multiplied with V: one part alone would round every weight to 8 bits, as much as the output's own rounding.
 // A candidate that a sequence did not select has weight exactly 0 there; if its V row holds an infinity or
 // NaN, 0 times that would still spoil the sum, so a tile with such a value is added up in plain
 // arithmetic that leaves weights of 0 out.
@@ -534,8 +534,8 @@ cudaError_t launch_cand(const PagedPlan& P, const void* Q, void* ws, cudaStream_
   const cudaError_t e = ensure_smem_limit(paged_cand_kernel<D, R>, cand_smem<D>());
   if (e != cudaSuccess) return e;
   return launch_after(
-      paged_cand_kernel<D, R>, dim3(P.n_psplit, P.H, (P.B + 16 * R - 1) / (16 * R)), cand_threads<R>(), cand_smem<D>(), s, 1,
-      (const uint16_t*)Q, (const uint16_t*)P.K, (const uint16_t*)P.V, ws_ptr<int4>(ws, P.off_rows),
+      paged_cand_kernel<D, R>, dim3(P.n_psplit, P.H, (P.B + 16 * R - 1) / (16 * R)), cand_threads<R>(), cand_smem<D>(),
+      s, 1, (const uint16_t*)Q, (const uint16_t*)P.K, (const uint16_t*)P.V, ws_ptr<int4>(ws, P.off_rows),
       ws_ptr<int32_t>(ws, P.off_crow), ws_ptr<int2>(ws, P.off_cent), ws_ptr<float>(ws, P.off_part), P.B, P.H, P.Hkv,
       P.page_shift, P.n_pages << P.page_shift, P.cand_len, P.cand_split, P.n_psplit + P.n_split, P.scale);
 }

@@ -51,7 +51,9 @@ DMA_DEVINL void wg_sync(int w) {
 }
 
 // Byte offset of 16-byte chunk c of row r in an operand tile of 128 rows.
-DMA_DEVINL uint32_t ct_at(int r, int c) { return (uint32_t)((c >> 3) * (kCtTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)); }
+DMA_DEVINL uint32_t ct_at(int r, int c) {
+  return (uint32_t)((c >> 3) * (kCtTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
 
 template <int KK, int NK> DMA_DEVINL void qk_steps(uint32_t d, uint64_t dq, uint64_t dk, uint32_t id) {
   if constexpr (KK < NK) {
@@ -199,7 +201,8 @@ paged_cand_tc_kernel(const uint16_t* Q, const uint16_t* K, const uint16_t* V, co
         const uint32_t key[4] = {key4.x, key4.y, key4.z, key4.w};
         const float dl[4] = {dl4.x, dl4.y, dl4.z, dl4.w};
 #pragma unroll
-        for (int v = 0; v < 4; ++v) z[u + v] = key[v] > floor ? fmaf(__uint_as_float(x[u + v]), scale, dl[v]) : -INFINITY;
+        for (int v = 0; v < 4; ++v)
+          z[u + v] = key[v] > floor ? fmaf(__uint_as_float(x[u + v]), scale, dl[v]) : -INFINITY;
         if (some)
 #pragma unroll
           for (int v = 0; v < 4; ++v)
@@ -321,8 +324,9 @@ paged_cand_tc_kernel(const uint16_t* Q, const uint16_t* K, const uint16_t* V, co
             if (p != 0.f) {
 #pragma unroll
               for (int u = 0; u < 4; ++u) {
-                o[2 * u] = __float_as_uint(fmaf(p, __uint_as_float(vw[u] << 16), __uint_as_float(o[2 * u])));
-                o[2 * u + 1] = __float_as_uint(fmaf(p, __uint_as_float(vw[u] & 0xffff0000u), __uint_as_float(o[2 * u + 1])));
+                const float v0 = __uint_as_float(vw[u] << 16), v1 = __uint_as_float(vw[u] & 0xffff0000u);
+                o[2 * u] = __float_as_uint(fmaf(p, v0, __uint_as_float(o[2 * u])));
+                o[2 * u + 1] = __float_as_uint(fmaf(p, v1, __uint_as_float(o[2 * u + 1])));
               }
             }
           }
@@ -402,8 +406,8 @@ paged_cand_tc_kernel(const uint16_t* Q, const uint16_t* K, const uint16_t* V, co
 template <int D> cudaError_t launch_d(const PagedPlan& P, const void* Q, void* ws, cudaStream_t s) {
   const cudaError_t e = ensure_smem_limit(paged_cand_tc_kernel<D>, CtSmem<D>::kBytes);
   if (e != cudaSuccess) return e;
-  return launch_after(paged_cand_tc_kernel<D>, dim3(P.n_psplit, P.H, (P.B + 63) / 64), kCtThreads, CtSmem<D>::kBytes, s, 1,
-                      (const uint16_t*)Q, (const uint16_t*)P.K, (const uint16_t*)P.V, ws_ptr<int4>(ws, P.off_rows),
+  return launch_after(paged_cand_tc_kernel<D>, dim3(P.n_psplit, P.H, (P.B + 63) / 64), kCtThreads, CtSmem<D>::kBytes, s,
+                      1, (const uint16_t*)Q, (const uint16_t*)P.K, (const uint16_t*)P.V, ws_ptr<int4>(ws, P.off_rows),
                       ws_ptr<int32_t>(ws, P.off_crow), ws_ptr<int2>(ws, P.off_cent), ws_ptr<float>(ws, P.off_part),
                       ws_ptr<int32_t>(ws, P.off_status), P.B, P.H, P.Hkv, P.page_shift, P.n_pages << P.page_shift,
                       P.cand_len, P.cand_split, P.n_psplit + P.n_split, P.scale);

@@ -27,11 +27,11 @@
 // rows that share an SM (58 % of the issue slots for 768 rows of up to 8192 values).  A CTA passes through
 // most of its code once, so instructions that have to come from memory first are a part of that chain: loops
 // over the resident keys are not unrolled and clusters of up to 4 have a kernel of their own, which takes 4 us
-// off a selection of 20 (8 sequences behind a prefix of 2048).  Measured: 8 sequences of
-// 65536 values, 32 heads, window 2048 (67 MB): 36 us, of which the first reading 13.5 (5 TB/s); without the
-// sieve 95.  48 sequences of up to 8192 values, 16 heads (12.6 MB): 25 us
-// (27 before the longest came first).  A prefix of 32768 values, 32 heads:
-// candidates 17 us, 64 sequences' own keys behind it 8 (25 more without rest_by_tail).
+// off a selection of 20 (8 sequences behind a prefix of 2048).  Measured, the kernel alone: 8 sequences of 65536
+// values, 32 heads, window 2048 (67 MB): 36 us, of which the first reading 13.5 (5 TB/s); without the sieve 95.  48
+// sequences of up to 8192 values, 16 heads (12.6 MB): 24 us.  A prefix of 32768 values, 32 heads: candidates 16 us, 64
+// sequences' own keys behind it 9 (25 more without rest_by_tail).  All of that with P.N the longest length: the
+// variants below are chosen by P.N, since lengths are not known when a kernel is launched.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -519,7 +519,8 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const int pos = i0 + min(from + u * 4, (ns - 1) & ~3);
-            f[u] = *reinterpret_cast<const float4*>(values_of(pages[(pos >> P.page_shift) - tab0]) + (pos & (page - 1)));
+            const float* at = values_of(pages[(pos >> P.page_shift) - tab0]);
+            f[u] = *reinterpret_cast<const float4*>(at + (pos & (page - 1)));
           }
         } else {
 #pragma unroll
@@ -532,10 +533,10 @@ paged_select_kernel(PagedPlan P, int32_t* __restrict__ rows, int32_t* __restrict
       for (int bt = warp; bt < nb; bt += NW) {
         fetch(bt + NW, from_next, f_next);
         const int left = ns - from;   // of a whole group 8 or more
-        unsigned own = (unsigned)(f[0].x >= least) | (unsigned)(f[0].y >= least) << 1 | (unsigned)(f[0].z >= least) << 2 |
-                       (unsigned)(f[0].w >= least) << 3 | (unsigned)(f[1].x >= least) << 4 |
-                       (unsigned)(f[1].y >= least) << 5 | (unsigned)(f[1].z >= least) << 6 |
-                       (unsigned)(f[1].w >= least) << 7;
+        unsigned own = (unsigned)(f[0].x >= least) | (unsigned)(f[0].y >= least) << 1 |
+                       (unsigned)(f[0].z >= least) << 2 | (unsigned)(f[0].w >= least) << 3 |
+                       (unsigned)(f[1].x >= least) << 4 | (unsigned)(f[1].y >= least) << 5 |
+                       (unsigned)(f[1].z >= least) << 6 | (unsigned)(f[1].w >= least) << 7;
         if (left < kPsGroup) own &= left > 0 ? (1u << left) - 1u : 0u;
         const int c = __popc(own);
         int incl = c;
@@ -960,7 +961,7 @@ cudaError_t launch_select(const PagedPlan& P, int n_rows, int n, void* ws, cudaS
   // clusters: stretches of at most 16384 values, and for few rows as many CTAs as there are SMs for (more
   // would wait: a cluster needs its SMs side by side), down to stretches of 2048 (32 rows of 32768 values in
   // four stretches rather than two: a sixth less time); short rows in large numbers go to small CTAs, more of
-  // which share an SM: 768 rows of up to 8192 values with 256 threads 25.9 us, with 512 30.7 (with 128, or
+  // which share an SM: 768 rows of up to 8192 values with 256 threads 26 us, with 512 31 (with 128, or
   // five CTAs of 256 an SM, 28); 2048 rows of some 2300 with 128 threads 9 us, with 512 25
   int C = 1;
   while (C < kPsMaxCluster && ((n + C - 1) / C > 16384 || (2 * n_rows * C <= sms && (n + C - 1) / C > 2048))) C *= 2;

@@ -10,8 +10,9 @@
 //
 // Both are bound by memory where there are many rows: every row is read once and written once, and nothing
 // else moves.  16384 tokens of 16 + 8 + 8 heads of 128 channels in bf16: forward 268 MB in 51 us (5.2 TB/s, 80 %
-// of the copy rate of 6.56), backward 436 MB in 90 us (4.9 TB/s, 74 %); the rest is issue slots (71 % of them
-// in the forward).  Forward with three CTAs an SM 53 us, with two 57; backward with two 92, with one 118.
+// of the copy rate of 6.56), backward 436 MB in 89 us (4.9 TB/s, 74 %); the rest is issue slots (71 % of them
+// in the forward).  In a graph from a cold L2, forward with three CTAs an SM as here 60 us, with two 64, with four
+// (64 registers) 67; backward with two as here 93, with one 122.
 // Small calls are bound by the way through the binding and the launch: 8 tokens in 8.4 us, 5 in a
 // graph (the backward has a second launch, of the weights' sums, that starts while the first ends).
 #include <math.h>
@@ -56,8 +57,9 @@ template <typename T> constexpr int bwd_rows() { return sizeof(T) == 2 ? 4 : 2; 
 // a row's gradient, and its input or (values) the gate's share
 template <typename T> using BwdRing = RowRing<sizeof(T) == 2 ? 3 : 4, bwd_rows<T>(), 2>;
 
-// Warps walk over the tokens in a fixed order, so the partial sums of the weights' gradients (float32
-// within a lane, at most a few thousand rows each) do not depend on scheduling.
+// Warps walk over the tokens in a fixed order, so the partial sums of the weights' gradients do not depend on
+// scheduling.  A lane adds up its own rows in float32, one in 4736 of all (148 SMs, 128 channels; one in 9472 of 64):
+// 55 for 16384 tokens of 16 heads, some 50 000 for as many as 180 GB hold, each addition off by 2^-24 at most.
 template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(kRwThreads, 2)
 prep_bwd_kernel(const __grid_constant__ PrepArgs a, int wt) {
@@ -75,7 +77,8 @@ prep_bwd_kernel(const __grid_constant__ PrepArgs a, int wt) {
     __syncthreads();
   };
   auto send = [&](const Walk& at, unsigned char* place) {
-    const int part = at.part(), h = at.within(part) * (RPW * U) + grp, heads = part == 0 ? a.H : a.Hkv, left = heads - h;
+    const int part = at.part(), h = at.within(part) * (RPW * U) + grp;
+    const int heads = part == 0 ? a.H : a.Hkv, left = heads - h;
     const size_t dense = (((size_t)at.b * heads + h) * at.N + at.n) * D + e, step = (size_t)RPW * at.N * D;
     const T* base = (const T*)a.grad[part];
 #pragma unroll
@@ -358,7 +361,8 @@ dma_status_t dma_prep_bwd(const dma_params_t* p, const dma_prep_t* r, const dma_
   dma_status_t e = prep_args(p, r, &a);
   if (e != DMA_OK) return e;
   const bool bf16 = p->dtype == DMA_BF16;
-  if (st == nullptr || gst == nullptr || !ok_ptr(dQ) || !ok_ptr(dK) || !ok_ptr(dq) || !ok_ptr(dk)) return DMA_ERR_INVALID_ARG;
+  if (st == nullptr || gst == nullptr || !ok_ptr(dQ) || !ok_ptr(dK) || !ok_ptr(dq) || !ok_ptr(dk))
+    return DMA_ERR_INVALID_ARG;
   if (r->q_weight != nullptr ? !ok_ptr(q) : !null_or_ok(q)) return DMA_ERR_INVALID_ARG;
   if (r->k_weight != nullptr ? !ok_ptr(k) : !null_or_ok(k)) return DMA_ERR_INVALID_ARG;
   if ((dv == nullptr) != (dV == nullptr) || (dv == nullptr && dV_gate != nullptr)) return DMA_ERR_INVALID_ARG;
