@@ -477,6 +477,8 @@ dma_status_t dma_paged_layout(const dma_params_t* p, const dma_pages_t* c, dma_p
  * length reaches it, or before it is described as one (with prefix 0): tokens of a sequence shorter than the
  * prefix are skipped and reported.  x is accumulated in float32.  The call is complete in the stream's order
  * like any other; it needs the workspace for its status word only.
+ * Of Q, dma_paged_attn takes one row a sequence, its last.  There is no call for several queries of a sequence
+ * over the pages: a prompt's own attention runs on dense tensors (dma_prep, dma_gate, dma_topk_mask, dma_attn_fwd).
  */
 dma_status_t dma_paged_append(const dma_params_t* p, const dma_pages_t* c, const dma_prep_t* r,
                               const dma_prep_strides_t* st, int32_t T, const int32_t* starts, const void* q,

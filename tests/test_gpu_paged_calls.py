@@ -228,3 +228,28 @@ def test_a_prompt_in_parts_is_the_prompt_at_once(H, Hkv, d, dtype):
     assert at == lens and c.dma.check_device_status(c.p, c.ws) == 0
     for x, y in zip(whole, (c.K, c.V, c.delta, Q)):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("name,N", [("rows", 5000), ("rows", 70_000), ("rows", 400_000), ("few_behind_prefix", 5000),
+                                    ("few_behind_prefix", 40_000), ("few_behind_prefix", 200_000),
+                                    ("many_behind_prefix", 3000), ("many_behind_prefix", 20_000),
+                                    ("many_behind_prefix", 120_000), ("long_rows", 80_000), ("long_rows", 600_000)])
+def test_a_limit_far_above_the_lengths(name, N):
+    """N chooses the kernels (other block sizes, clusters nearly all without a key, the sieve), not the results."""
+    c = _make(name)
+    torch, dma = c.torch, c.dma
+    per = -(-N // c.page)
+    table = torch.full((len(c.lens_host), per), -1, dtype=torch.int32, device="cuda")   # nothing behind a row's pages
+    table[:, :c.table.shape[1]] = c.table
+    c.table, c.N = table, N
+    c.p = dma.make_params(len(c.lens_host), c.H, c.Hkv, N, c.d, c.w, Nq=1, dtype=c.dtype)
+    c.c = dma.make_pages(c.p, c.K, c.V, c.delta, table, c.lens, prefix=c.prefix)
+    c.ws = dma.alloc_paged_workspace(c.p, c.c)
+    c.ws[256:].fill_(0xA5)
+    out = c.run()
+    torch.cuda.synchronize()
+    c.check_selection()
+    c.check(*out)
+    again = c.run(out[0])
+    for x, y in zip(out, again):
+        assert torch.equal(x, y)
